@@ -23,6 +23,14 @@ Allocating helpers with the pages' argument conventions:
     pack(cp_attn_out, cp_attn_lse, world_size)
     combine_pack(partial_outputs, partial_lses, world_size)   (split merge + pack in one pass)
     unpack_combine(recv_buf, return_lse=False, is_lse_base_on_e=True)
+
+The cache that the partial results come from (one rank's shard, paged; see the module ``paged``):
+    dcp_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc, ...)
+    paged_attention(q, k_cache, v_cache, block_table, seq_lens, ...)         -> result, lse
+    paged_attention_pack(q, k_cache, v_cache, block_table, seq_lens, world_size, ...)  -> send buffer
+    dcp_kv_weights(logits, global_lse, seq_lens, weights, ...)               (accumulated weights)
+    kv_evict(weights, k_cache, v_cache, block_table, seq_lens, new_block_table, keep, recent, ...)
+with dcp_paged_attention, dcp_paged_attention_pack and dcp_kv_evict taking caller-allocated outputs.
 """
 from __future__ import annotations
 
@@ -38,6 +46,8 @@ __all__ = [
     "dcp_combine_pack", "dcp_unpack_combine", "combine_pack", "dcp_last_error", "dcp_version", "dcp_wait_timeouts", "lse_weighted_combine", "lse_weighted_combine_varlen",
     "merge_dcp_outputs", "pack", "unpack_combine",
     "DTYPE_CODES",
+    "dcp_kv_append", "dcp_kv_evict", "dcp_kv_weights", "dcp_paged_attention", "dcp_paged_attention_pack", "kv_evict",
+    "paged_attention", "paged_attention_pack", "paged_attention_workspace",
 ]
 
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -95,6 +105,7 @@ def library() -> ctypes.CDLL:
                 lib.dcp_wait_timeouts.restype = _i32
                 lib.dcp_version.argtypes = []
                 lib.dcp_version.restype = _i32
+                paged.declare(lib)
                 _lib = lib
     return _lib
 
@@ -378,3 +389,9 @@ def unpack_combine(recv_buf: torch.Tensor, return_lse: bool = False, is_lse_base
     glse = torch.empty((B, Hr), dtype=torch.float32, device=recv_buf.device) if return_lse else None
     dcp_unpack_combine(recv_buf, result, glse, is_lse_base_on_e=is_lse_base_on_e, return_lse=return_lse)
     return (result, glse) if return_lse else result
+
+
+from . import paged  # noqa: E402
+from .paged import (dcp_kv_append, dcp_kv_evict, dcp_kv_weights, dcp_paged_attention,  # noqa: E402
+                    dcp_paged_attention_pack, kv_evict, paged_attention, paged_attention_pack,
+                    paged_attention_workspace)

@@ -1,0 +1,10 @@
+// dcp_paged_attention_fp32.cu -- the paged attention kernel instances for fp32 data.
+#include "dcp_paged_attention.cuh"
+
+namespace dcp_host {
+
+int32_t paged_attention_fp32(const dcp::AttentionArgs &a, cudaStream_t stream) {
+    return paged_attention<dcp::Fp32>(a, stream);
+}
+
+}  // namespace dcp_host
