@@ -81,6 +81,7 @@ struct AttentionArgs {
     int64_t logits_sb, logits_sh;
     int32_t logits_cap;
     int32_t B, H, group;  // group = H / kv.heads
+    int32_t row_blocks, head_blocks;  // passes per group (set at launch), and over all key heads
     int32_t pack_hr;      // heads per rank of the packed send buffer, 0 = plain result
     FastDiv pack_div;
     float scale;
@@ -125,7 +126,9 @@ int32_t paged_attention_bf16(const dcp::AttentionArgs &a, cudaStream_t stream);
 int32_t paged_attention_fp16(const dcp::AttentionArgs &a, cudaStream_t stream);
 int32_t paged_attention_fp32(const dcp::AttentionArgs &a, cudaStream_t stream);
 // Bytes of workspace the launches above use on the current device.
-int64_t paged_attention_workspace(int32_t group, int32_t head_dim, int32_t dtype);
+int64_t attention_workspace_bf16(int32_t group, int32_t head_dim);
+int64_t attention_workspace_fp16(int32_t group, int32_t head_dim);
+int64_t attention_workspace_fp32(int32_t group, int32_t head_dim);
 int32_t kv_append(const dcp::AppendArgs &a, cudaStream_t stream);
 int32_t kv_weights(const dcp::WeightsArgs &a, cudaStream_t stream);
 int32_t kv_evict(const dcp::EvictArgs &a, cudaStream_t stream);

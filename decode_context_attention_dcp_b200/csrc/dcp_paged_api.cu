@@ -12,6 +12,7 @@ using dcp_host::fail;
 using dcp_host::ok;
 
 constexpr int64_t kLimit = int64_t(1) << 31;
+constexpr int64_t kMaxPositions = kLimit - 1024;  // positions and tile ends are ints in the kernels
 
 int elem_size(int32_t dtype) { return dtype == DCP_FP32 ? 4 : dtype == DCP_BF16 || dtype == DCP_FP16 ? 2 : 0; }
 
@@ -23,6 +24,14 @@ dcp::FastDiv fast_div(uint64_t d) {
     f.magic = d <= 1 ? 0 : (uint64_t)(((one << 64) + d - 1) / d);
     f.d = (uint32_t)d;
     return f;
+}
+
+int64_t attention_workspace(int32_t group, int32_t head_dim, int32_t dtype) {
+    switch (dtype) {
+        case DCP_BF16: return dcp_host::attention_workspace_bf16(group, head_dim);
+        case DCP_FP16: return dcp_host::attention_workspace_fp16(group, head_dim);
+        default: return dcp_host::attention_workspace_fp32(group, head_dim);
+    }
 }
 
 // `used`: the call reads the block table (it has requests), so its pointers must be there.
@@ -38,8 +47,8 @@ int32_t check_cache(const char *fn, const dcp_paged_kv *kv, bool used, dcp::Page
     if (kv->heads < 1) return fail(DCP_ERR_INVALID_ARG, "%s: key head count %d < 1", fn, (int)kv->heads);
     if (kv->page_size < 1) return fail(DCP_ERR_INVALID_ARG, "%s: page size %d < 1", fn, (int)kv->page_size);
     if (kv->num_pages < 0 || kv->max_pages < 0) return fail(DCP_ERR_INVALID_ARG, "%s: negative page count", fn);
-    if (kv->max_pages >= kLimit || kv->max_pages * kv->page_size >= kLimit)
-        return fail(DCP_ERR_INVALID_ARG, "%s: a block table row names 2^31 positions or more", fn);
+    if (kv->max_pages >= kLimit || kv->max_pages * kv->page_size >= kMaxPositions)
+        return fail(DCP_ERR_INVALID_ARG, "%s: a block table row names 2^31 - 1024 positions or more", fn);
     const int64_t st[7] = {kv->k_stride_page, kv->k_stride_slot, kv->k_stride_head, kv->v_stride_page,
                            kv->v_stride_slot, kv->v_stride_head, kv->table_stride};
     for (int i = 0; i < 7; ++i)
@@ -125,7 +134,7 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
         return fail(DCP_ERR_MISALIGNED, "%s: the query and the result must be 16-byte aligned", fn);
     if (!aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(logits, 4))
         return fail(DCP_ERR_MISALIGNED, "%s: seq_lens, lse and logits must be 4-byte aligned", fn);
-    const int64_t need = dcp_host::paged_attention_workspace((int32_t)(H / kv->heads), kv->head_dim, kv->dtype);
+    const int64_t need = attention_workspace((int32_t)(H / kv->heads), kv->head_dim, kv->dtype);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
             return fail(DCP_ERR_INVALID_ARG, "%s: the workspace holds %lld bytes, %lld are needed", fn,
@@ -166,7 +175,7 @@ int64_t dcp_paged_attention_workspace(int64_t H, int32_t heads, int32_t head_dim
     if (heads < 1 || H < 1 || H >= kLimit || H % heads || head_dim < 1 || head_dim > DCP_MAX_PAGED_DIM ||
         elem_size(dtype) == 0)
         return -1;
-    return dcp_host::paged_attention_workspace((int32_t)(H / heads), head_dim, dtype);
+    return attention_workspace((int32_t)(H / heads), head_dim, dtype);
 }
 
 int32_t dcp_paged_attention(const dcp_paged_kv *kv, const void *q, const int32_t *seq_lens, void *result, float *lse,
@@ -320,9 +329,3 @@ int32_t dcp_kv_evict(const dcp_paged_kv *src, const dcp_paged_kv *dst, const int
 }
 
 }  // extern "C"
-
-namespace dcp_host {
-
-int64_t paged_attention_workspace(int32_t, int32_t, int32_t) { return 0; }
-
-}  // namespace dcp_host

@@ -7,4 +7,8 @@ int32_t paged_attention_fp16(const dcp::AttentionArgs &a, cudaStream_t stream) {
     return paged_attention<dcp::Fp16>(a, stream);
 }
 
+int64_t attention_workspace_fp16(int32_t group, int32_t head_dim) {
+    return attention_workspace<dcp::Fp16>(group, head_dim);
+}
+
 }  // namespace dcp_host

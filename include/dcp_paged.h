@@ -58,7 +58,7 @@ extern "C" {
  *
  * Requirements: dtype a dcp_dtype; head_dim in [1, DCP_MAX_PAGED_DIM] with rows a multiple of
  * 16 bytes; heads >= 1; page_size >= 1; num_pages >= 0; max_pages >= 0; max_pages * page_size
- * < 2^31; k and v 16-byte aligned; strides >= 0 and multiples of 16 bytes; block_table 4-byte
+ * < 2^31 - 1024; k and v 16-byte aligned; strides >= 0 and multiples of 16 bytes; block_table 4-byte
  * aligned, entry (b, j) at b*table_stride + j.
  */
 typedef struct {
@@ -91,8 +91,10 @@ int64_t dcp_paged_attention_workspace(int64_t H, int32_t heads, int32_t head_dim
  *   result = sum_p exp(x_p - m) v_p / sum_p exp(x_p - m)      (fp32 sums, one rounding)
  *   lse    = ln(sum_p exp(x_p - m)) + m                       (log2 in base 2)
  * A request without held positions gives 0 and -inf, which dcp_lse_combine then leaves out.
- * A position whose logit is -inf adds nothing, a row whose logits are all -inf counts as empty.
- * For 16-bit types exp(x_p - m) is carried into the product with v as two 16-bit parts.
+ * A position whose logit is -inf adds nothing, a row whose logits are all -inf counts as empty
+ * (16-bit types; a row that meets a non-finite fp32 key or value is NaN).
+ * For 16-bit types exp(x_p - m) is carried into the product with v as two 16-bit parts; fp32
+ * products are formed from two tf32 parts of each factor (2^-20 of the product).
  *
  * q           [B, H, head_dim] of kv->dtype; element (b, h, d) at b*q_stride_b + h*q_stride_h + d.
  * seq_lens    [B] int32, device.
