@@ -727,9 +727,7 @@ int32_t launch_attention(dcp::AttentionArgs a, cudaStream_t stream) {
     using T = typename S::T;
     static InstanceCache cache;
     const char *fn = "dcp_paged_attention";
-    if (!reserve_smem(dcp::attention_stream_kernel<S>, cache, S::kSmem) ||
-        cudaFuncSetAttribute(dcp::attention_stream_kernel<S>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+    if (!reserve_smem(dcp::attention_stream_kernel<S>, cache, S::kSmem))
         return fail(DCP_ERR_CUDA, "%s: cannot reserve shared memory", fn);
     a.row_blocks = (a.group + S::kRows - 1) / S::kRows;
     a.head_blocks = a.kv.heads * a.row_blocks;

@@ -1,61 +1,197 @@
 // dcp_paged_cache.cu -- the row movers of the paged cache: append, accumulated weights, eviction.
+//
+// None of them computes much: append and the moves of an eviction are copies, the weights one
+// exp per logit.  They are bound by HBM where they are long and by the chain of dependent reads
+// (request, length, page, row) where they are short, so each kernel first finds the places of a
+// block's rows with one thread per row and then copies with every thread, several 16-byte
+// loads in flight each.
 #include "dcp_paged.cuh"
+
+#include <cooperative_groups.h>
 
 namespace dcp {
 
+namespace cg = cooperative_groups;
+
+constexpr int kCopyThreads = 256;
+
+// Words of a K and a V row, source and destination; k_from < 0: nothing to copy.
+struct RowMove {
+    int64_t k_from, v_from, k_to, v_to;
+};
+
+// Copies the rows listed in `moves` (in shared memory): 16-byte chunk c of row r by thread
+// (r * chunks + c) mod kCopyThreads, U chunks of K and of V in flight per thread.
+template <int U>
+__device__ __forceinline__ void copy_rows(const RowMove *moves, int rows, FastDiv chunks, const uint32_t *k_src,
+                                          const uint32_t *v_src, uint32_t *k_dst, uint32_t *v_dst) {
+    const int items = rows * (int)chunks.d;
+    for (int i0 = threadIdx.x; i0 < items; i0 += U * kCopyThreads) {
+        uint4 k[U], v[U];
+        int64_t k_to[U], v_to[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kCopyThreads;
+            k_to[u] = -1;
+            if (i < items) {
+                const int r = (int)chunks.div((uint32_t)i), w = (i - r * (int)chunks.d) * 4;
+                const RowMove mv = moves[r];
+                if (mv.k_from >= 0) {
+                    k[u] = *reinterpret_cast<const uint4 *>(k_src + mv.k_from + w);
+                    v[u] = *reinterpret_cast<const uint4 *>(v_src + mv.v_from + w);
+                    k_to[u] = mv.k_to + w;
+                    v_to[u] = mv.v_to + w;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k_to[u] >= 0) {
+                *reinterpret_cast<uint4 *>(k_dst + k_to[u]) = k[u];
+                *reinterpret_cast<uint4 *>(v_dst + v_to[u]) = v[u];
+            }
+    }
+}
+
 // ---- append -----------------------------------------------------------------------------------
-// One warp per (token, key head): finds the token's request, its position and slot, and copies
-// the key and value row.
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendArgs a) {
-    const uint32_t unit = blockIdx.x * 8 + threadIdx.x / 32;
-    if (unit >= (uint32_t)a.T * (uint32_t)a.kv.heads) return;
-    const uint32_t t = unit / (uint32_t)a.kv.heads, h = unit - t * a.kv.heads, lane = threadIdx.x & 31;
-    // the last request that starts at or before t
-    int lo = 0, hi = a.num_reqs;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.qsl[mid] <= (int32_t)t) lo = mid + 1; else hi = mid;
+constexpr int kAppendRows = 64;  // rows a block places at a time
+
+// The last request that starts at or before token t, or -1: the 32 lanes probe 32 starts at once,
+// first those around the request that the token's share of all tokens points to (exact for plain
+// decode), then ever smaller ranges.  Reads stay inside qsl[0 .. num_reqs - 1].
+__device__ __forceinline__ int request_of(const AppendArgs &a, int t) {
+    const int lane = threadIdx.x & 31, R = a.num_reqs;
+    int lo = 0, hi = R;  // the answer + 1, the number of starts <= t, lies in [lo, hi]
+    int64_t guess = (int64_t)t * R / a.T - 15;
+    guess = guess < 0 ? 0 : guess;
+    {
+        const int64_t i = guess + lane;
+        const bool in = i < R;
+        const unsigned some = __ballot_sync(0xffffffffu, in);
+        const unsigned le = __ballot_sync(0xffffffffu, in && a.qsl[in ? i : 0] <= t);
+        // starts are non-decreasing: `le` is a prefix of `some`
+        const int n = __popc(le);
+        if (n) lo = (int)guess + n;
+        else hi = (int)guess;
+        if (n && n < __popc(some)) hi = lo;
     }
-    const int r = lo - 1;
-    if (r < 0) return;
-    const int64_t left = (int64_t)a.qsl[r + 1] - t;
-    if (left <= 0) return;
-    const int64_t pos = (int64_t)a.seq_lens[r] - left;
-    if (pos < 0) return;
-    uint32_t p = (uint32_t)pos;
-    if (!a.sh.one) {
-        const uint32_t run = a.sh.run.div(p), round = a.sh.count.div(run);
-        if ((int32_t)(run - round * a.sh.count.d) != a.sh.shard) return;
-        p = round * a.sh.run.d + (p - run * a.sh.run.d);
+    for (int round = 0; round < 32 && lo < hi; ++round) {
+        const int64_t span = hi - lo;
+        const int64_t i = lo + (span * (lane + 1)) / 33;  // lo <= i < hi
+        const int n = __popc(__ballot_sync(0xffffffffu, a.qsl[i] <= t));
+        const int nlo = n == 0 ? lo : (int)(lo + (span * n) / 33) + 1;
+        hi = n == 32 ? hi : (int)(lo + (span * (n + 1)) / 33);
+        lo = nlo;
     }
-    if (p >= (uint32_t)a.kv.capacity) return;
-    int64_t page;
-    uint32_t slot;
-    if (!locate(a.kv, a.kv.table + r * a.kv.table_stride, p, page, slot)) return;
-    const uint32_t *ks = a.k_new + t * a.k_st_w + h * a.k_sh_w, *vs = a.v_new + t * a.v_st_w + h * a.v_sh_w;
-    uint32_t *kd = a.kv.k + page * a.kv.k_page_w + slot * a.kv.k_slot_w + h * a.kv.k_head_w;
-    uint32_t *vd = a.kv.v + page * a.kv.v_page_w + slot * a.kv.v_slot_w + h * a.kv.v_head_w;
-    for (int c = lane * 4; c < a.kv.data_w; c += 128) {
-        const Words<4> k = load_stream<4>(ks + c), v = load_stream<4>(vs + c);
-        store_words<4>(kd + c, k);
-        store_words<4>(vd + c, v);
+    return lo - 1;
+}
+
+// A block takes `per` tokens at a time (all heads, at most kAppendRows rows): each warp finds the
+// slots of its tokens, then the whole block copies the rows.
+__global__ void __launch_bounds__(kCopyThreads) kv_append_kernel(const __grid_constant__ AppendArgs a, int per,
+                                                                 FastDiv chunks) {
+    __shared__ RowMove moves[kAppendRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int heads = a.kv.heads;
+    // rows of one token in pieces of at most kAppendRows heads
+    const int pieces = (heads - 1) / kAppendRows + 1;
+    const int64_t groups = ((int64_t)(a.T - 1) / per + 1) * pieces;
+    for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
+        const int64_t tg = g / pieces;
+        const int h0 = (int)(g - tg * pieces) * kAppendRows, hn = min(heads - h0, kAppendRows);
+        const int t0 = (int)(tg * per), tn = (int)min((int64_t)per, (int64_t)a.T - t0);
+        for (int i = warp; i < tn; i += kCopyThreads / 32) {
+            const int t = t0 + i, r = request_of(a, t);
+            RowMove mv{-1, 0, 0, 0};
+            if (r >= 0) {
+                const int64_t left = (int64_t)a.qsl[r + 1] - t, pos = (int64_t)a.seq_lens[r] - left;
+                bool mine = left > 0 && pos >= 0;
+                uint32_t p = (uint32_t)pos;
+                if (mine && !a.sh.one) {
+                    const uint32_t run = a.sh.run.div(p), round = a.sh.count.div(run);
+                    mine = (int32_t)(run - round * a.sh.count.d) == a.sh.shard;
+                    p = round * a.sh.run.d + (p - run * a.sh.run.d);
+                }
+                int64_t page = 0;
+                uint32_t slot = 0;
+                if (mine && p < (uint32_t)a.kv.capacity &&
+                    locate(a.kv, a.kv.table + r * a.kv.table_stride, p, page, slot)) {
+                    mv.k_from = t * a.k_st_w;
+                    mv.v_from = t * a.v_st_w;
+                    mv.k_to = page * a.kv.k_page_w + slot * a.kv.k_slot_w;
+                    mv.v_to = page * a.kv.v_page_w + slot * a.kv.v_slot_w;
+                }
+            }
+            for (int h = lane; h < hn; h += 32) {
+                RowMove m = mv;
+                if (m.k_from >= 0) {
+                    m.k_from += (h0 + h) * a.k_sh_w;
+                    m.v_from += (h0 + h) * a.v_sh_w;
+                    m.k_to += (h0 + h) * a.kv.k_head_w;
+                    m.v_to += (h0 + h) * a.kv.v_head_w;
+                }
+                moves[i * hn + h] = m;
+            }
+        }
+        __syncthreads();
+        copy_rows<4>(moves, tn * hn, chunks, a.k_new, a.v_new, a.kv.k, a.kv.v);
+        __syncthreads();
     }
 }
 
 // ---- accumulated weights ----------------------------------------------------------------------
-// One CTA per (request, key head), threads along the positions.
-__global__ void __launch_bounds__(256) kv_weights_kernel(const __grid_constant__ WeightsArgs a) {
-    const int j = blockIdx.x % a.heads, b = blockIdx.x / a.heads;
+constexpr int kWeighThreads = 256;
+
+// w[p] += sum_h exp(x[h][p] - l[h]): a block takes one row (request, key head) and every
+// `splits`-th stretch of 1024 of its positions; a thread owns 4 positions (adjacent ones and 16-byte
+// accesses where VEC, i.e. all rows start on 16 bytes).
+template <bool VEC>
+__global__ void __launch_bounds__(kWeighThreads) kv_weights_kernel(const __grid_constant__ WeightsArgs a, int splits) {
+    const int row = blockIdx.x / splits, part = blockIdx.x - row * splits;
+    const int b = row / a.heads, j = row - b * a.heads;
     const int n = local_length(a.sh, a.seq_lens[b], a.cap);
-    for (int p = threadIdx.x; p < n; p += 256) {
-        float w = 0.f;
-        for (int g = 0; g < a.group; ++g) {
-            const int h = j * a.group + g;
-            const float l = a.lse[b * a.lse_sb + h * a.lse_sh];
-            const float x = a.logits[b * a.logits_sb + h * a.logits_sh + p];
-            if (isfinite(l)) w += a.base_e ? expf(x - l) : exp2f(x * 1.44269504088896340736f - l);
+    const float *x0 = a.logits + b * a.logits_sb + (int64_t)j * a.group * a.logits_sh;
+    const float *l0 = a.lse + b * a.lse_sb + (int64_t)j * a.group * a.lse_sh;
+    float *w = a.weights + b * a.w_sb + j * a.w_sh;
+    for (int64_t p0 = (int64_t)part * (4 * kWeighThreads); p0 < n; p0 += (int64_t)splits * (4 * kWeighThreads)) {
+        const int64_t p = p0 + (VEC ? threadIdx.x * 4 : threadIdx.x);
+        constexpr int STEP = VEC ? 1 : kWeighThreads;
+        if (p >= n) continue;
+        const bool whole = p + 3 * STEP < n;
+        float old[4], add[4] = {0.f, 0.f, 0.f, 0.f};
+        if (VEC && whole) {
+            const float4 o = *reinterpret_cast<const float4 *>(w + p);
+            old[0] = o.x, old[1] = o.y, old[2] = o.z, old[3] = o.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) old[e] = p + e * STEP < n ? w[p + e * STEP] : 0.f;
         }
-        a.weights[b * a.w_sb + j * a.w_sh + p] += w;
+#pragma unroll 4
+        for (int g = 0; g < a.group; ++g) {
+            const float l = l0[g * a.lse_sh];
+            const float *x = x0 + g * a.logits_sh + p;
+            float v[4];
+            if (VEC && whole) {
+                const float4 q = __ldcs(reinterpret_cast<const float4 *>(x));
+                v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = p + e * STEP < n ? __ldcs(x + e * STEP) : 0.f;
+            }
+            if (isfinite(l)) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    add[e] += a.base_e ? expf(v[e] - l) : exp2f(fmaf(v[e], 1.44269504088896340736f, -l));
+            }
+        }
+        if (VEC && whole) {
+            *reinterpret_cast<float4 *>(w + p) =
+                make_float4(old[0] + add[0], old[1] + add[1], old[2] + add[2], old[3] + add[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (p + e * STEP < n) w[p + e * STEP] = old[e] + add[e];
+        }
     }
 }
 
@@ -67,97 +203,198 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One CTA per (request, key head): the threshold key by four passes of 8 bits over the weights,
-// then an ordered pass that writes the kept positions and their weights.
-__global__ void __launch_bounds__(256) kv_select_kernel(const __grid_constant__ EvictArgs a) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t s_prefix, s_need, scan[9], s_ties[9];
-    const int j = blockIdx.x % a.src.heads, b = blockIdx.x / a.src.heads, tid = threadIdx.x;
+constexpr int kSelectThreads = 1024;
+constexpr int kBins = 2048;
+
+// Exclusive prefix and total of one value per thread over the block; `sums` is shared scratch.
+__device__ __forceinline__ uint64_t block_prefix(uint64_t mine, uint64_t *sums, uint64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    __syncthreads();  // the scratch may still be read from the last call
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    uint64_t s = sums[lane];
+    uint64_t all = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += x;
+    }
+    total = __shfl_sync(0xffffffffu, all, 31);
+    return upto - mine + __shfl_sync(0xffffffffu, all - s, warp);
+}
+
+// One cluster per (request, key head).  A thread holds KPT adjacent weights; positions past the
+// cluster's CTAs * 1024 * KPT are handled in further rounds that read them again.
+//   threshold: the key of the last kept position, 11 + 11 + 10 bits, one shared-memory histogram
+//   per pass (summed over the cluster through distributed shared memory) and a suffix scan;
+//   output: keys above it and the first ties are placed by a prefix sum in position order.
+template <int KPT>
+__global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_constant__ EvictArgs a) {
+    __shared__ uint32_t hist[3][kBins];
+    __shared__ uint64_t sums[32];
+    __shared__ uint64_t s_total[2];
+    __shared__ uint32_t s_digit, s_need;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), tid = threadIdx.x;
+    const int row = blockIdx.x / ctas, b = row / a.src.heads, j = row - b * a.src.heads;
     const float *w = a.weights + b * a.w_sb + j * a.w_sh;
     float *nw = a.new_weights + b * a.nw_sb + j * a.nw_sh;
-    int32_t *kept = a.kept + (int64_t)blockIdx.x * a.keep;
+    int32_t *kept = a.kept + (int64_t)row * a.keep;
     const int cap = a.src.capacity < a.cap ? a.src.capacity : a.cap;
     const int n = local_length(a.sh, a.seq_lens[b], cap);
     const int m = n < a.keep ? n : a.keep;
-    if (j == 0 && tid == 0) a.new_lens[b] = m;
-    const int body = n > a.keep ? n - a.recent : 0;  // positions that compete
-    uint32_t prefix = 0, need = (uint32_t)(a.keep - a.recent);
-    if (body && need) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            hist[tid] = 0;
-            __syncthreads();
-            for (int p = tid; p < body; p += 256) {
-                const uint32_t key = weight_key(w[p]);
-                if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1u);
+    if (j == 0 && rank == 0 && tid == 0) a.new_lens[b] = m;
+    const bool full = n <= a.keep;
+    const int body = full ? 0 : n - a.recent;            // positions that compete
+    const uint32_t want = full ? 0 : (uint32_t)(a.keep - a.recent);
+    const int64_t round = (int64_t)ctas * kSelectThreads * KPT;
+    const int64_t mine = ((int64_t)rank * kSelectThreads + tid) * KPT;
+
+    auto load = [&](int64_t p, uint32_t *key) {
+        if (p + KPT <= body && ((reinterpret_cast<uintptr_t>(w + p)) & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < KPT; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(w + p + i);
+                key[i] = weight_key(v.x), key[i + 1] = weight_key(v.y);
+                key[i + 2] = weight_key(v.z), key[i + 3] = weight_key(v.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) key[i] = p + i < body ? weight_key(w[p + i]) : 0u;
+        }
+    };
+    uint32_t first[KPT];
+    uint32_t prefix = 0, need = want;
+    if (want) {
+        load(mine, first);
+        for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            for (int64_t p0 = mine; p0 < body; p0 += round) {
+                uint32_t again[KPT];
+                if (p0 != mine) load(p0, again);
+#pragma unroll
+                for (int i = 0; i < KPT; ++i) {
+                    const uint32_t key = p0 == mine ? first[i] : again[i];
+                    const bool in = p0 + i < body && (pass == 0 || (key >> (shift + bits)) == (prefix >> (shift + bits)));
+                    if (in) atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1u)], 1u);
+                }
+            }
+            cluster.sync();
+            // bins in descending order: thread t holds bins kBins - 1 - 2t and the one below
+            uint32_t c[2] = {0, 0};
+            const int top = kBins - 1 - 2 * tid;
+            for (int r = 0; r < ctas; ++r) {
+                const uint32_t *other = ctas == 1 ? &hist[pass][0] : cluster.map_shared_rank(&hist[pass][0], r);
+                c[0] += other[top];
+                c[1] += other[top - 1];
+            }
+            uint64_t total;
+            const uint32_t above = (uint32_t)block_prefix(c[0] + c[1], sums, total);
+            if (above < need && need <= above + c[0] + c[1]) {
+                const bool low = need > above + c[0];
+                s_digit = (uint32_t)(low ? top - 1 : top);
+                s_need = need - above - (low ? c[0] : 0);
             }
             __syncthreads();
-            if (tid == 0) {
-                int d = 255;
-                while (d > 0 && hist[d] < need) need -= hist[d--];
-                s_prefix = prefix | ((uint32_t)d << shift);
-                s_need = need;
-            }
-            __syncthreads();
-            prefix = s_prefix;
+            prefix |= s_digit << shift;
             need = s_need;
         }
     }
-    // keys above `prefix` are kept, and the first `need` equal to it
-    uint32_t out = 0, ties = 0;
-    for (int p0 = 0; p0 < n; p0 += 256) {
-        const int p = p0 + tid;
-        const bool in = p < n;
-        const float x = in ? w[p] : 0.f;
-        const uint32_t key = weight_key(x);
-        const bool tie = in && p < body && key == prefix;
-        const unsigned tm = __ballot_sync(0xffffffffu, tie);
-        if ((tid & 31) == 0) s_ties[tid / 32] = __popc(tm);
-        __syncthreads();
-        uint32_t before = ties + __popc(tm & ((1u << (tid & 31)) - 1u)), all = 0;
-        for (int i = 0; i < 8; ++i) {
-            if (i < tid / 32) before += s_ties[i];
-            all += s_ties[i];
+    // keys above `prefix` are kept, and the first `need` that equal it
+    uint64_t before = 0;  // (ties << 32 | above) in earlier rounds
+    if (want)
+    for (int64_t q = 0; q < body; q += round) {
+        const int64_t p = q + mine;
+        uint32_t key[KPT];
+        uint64_t count = 0;
+        if (q == 0) {
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) key[i] = first[i];
+        } else {
+            load(p, key);
         }
-        const bool keep = in && (p >= body || (a.keep > a.recent && (key > prefix || (tie && before < need))));
-        const unsigned km = __ballot_sync(0xffffffffu, keep);
-        if ((tid & 31) == 0) scan[tid / 32] = __popc(km);
-        __syncthreads();
-        uint32_t at = out + __popc(km & ((1u << (tid & 31)) - 1u)), total = 0;
-        for (int i = 0; i < 8; ++i) {
-            if (i < tid / 32) at += scan[i];
-            total += scan[i];
+#pragma unroll
+        for (int i = 0; i < KPT; ++i)
+            if (p + i < body) count += key[i] > prefix ? 1ull : key[i] == prefix ? 1ull << 32 : 0ull;
+        uint64_t total;
+        uint64_t at = before + block_prefix(count, sums, total);
+        if (ctas > 1) {
+            if (tid == 0) s_total[0] = total;
+            cluster.sync();
+            uint64_t all = 0;
+            for (int r = 0; r < ctas; ++r) {
+                const uint64_t x = *cluster.map_shared_rank(&s_total[0], r);
+                if (r < rank) at += x;
+                all += x;
+            }
+            cluster.sync();
+            total = all;
         }
-        if (keep) {
-            kept[at] = p;
-            nw[at] = x;
+        before += total;
+        uint32_t above = (uint32_t)at, ties = (uint32_t)(at >> 32);
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            if (p + i >= body) break;
+            const bool gt = key[i] > prefix, eq = key[i] == prefix;
+            if (gt || (eq && ties < need)) {
+                const uint32_t to = above + (ties < need ? ties : need);
+                kept[to] = (int32_t)(p + i);
+                nw[to] = w[p + i];
+            }
+            above += gt;
+            ties += eq;
         }
-        ties += all;
-        out += total;
-        __syncthreads();
     }
-    for (int i = m + tid; i < a.keep; i += 256) kept[i] = -1;
-    for (int i = m + tid; i < a.new_cap; i += 256) nw[i] = 0.f;
+    // the last positions, then what is left of the outputs
+    const int step = ctas * kSelectThreads, id = rank * kSelectThreads + tid;
+    for (int64_t p = (int64_t)body + id; p < n; p += step) {
+        const int64_t to = (int64_t)want + (p - body);
+        kept[to] = (int32_t)p;
+        nw[to] = w[p];
+    }
+    for (int64_t i = (int64_t)m + id; i < a.keep; i += step) kept[i] = -1;
+    for (int64_t i = (int64_t)m + id; i < a.new_cap; i += step) nw[i] = 0.f;
+    if (ctas > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-// One warp per kept row: its key and value row from the source page to the destination page.
-__global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ EvictArgs a) {
-    const int b = blockIdx.y / a.src.heads, h = blockIdx.y % a.src.heads, lane = threadIdx.x & 31;
-    const int i = blockIdx.x * 8 + threadIdx.x / 32;
-    if (i >= a.keep) return;
-    const int32_t p = a.kept[(int64_t)blockIdx.y * a.keep + i];
-    if (p < 0) return;
-    int64_t sp, dp;
-    uint32_t ss, ds;
-    if (!locate(a.src, a.src.table + b * a.src.table_stride, p, sp, ss)) return;
-    if (!locate(a.dst, a.dst.table + b * a.dst.table_stride, i, dp, ds)) return;
-    const uint32_t *ks = a.src.k + sp * a.src.k_page_w + ss * a.src.k_slot_w + h * a.src.k_head_w;
-    const uint32_t *vs = a.src.v + sp * a.src.v_page_w + ss * a.src.v_slot_w + h * a.src.v_head_w;
-    uint32_t *kd = a.dst.k + dp * a.dst.k_page_w + ds * a.dst.k_slot_w + h * a.dst.k_head_w;
-    uint32_t *vd = a.dst.v + dp * a.dst.v_page_w + ds * a.dst.v_slot_w + h * a.dst.v_head_w;
-    for (int c = lane * 4; c < a.src.data_w; c += 128) {
-        const uint4 k = *reinterpret_cast<const uint4 *>(ks + c), v = *reinterpret_cast<const uint4 *>(vs + c);
-        *reinterpret_cast<uint4 *>(kd + c) = k;
-        *reinterpret_cast<uint4 *>(vd + c) = v;
+constexpr int kMoveRows = 64;  // kept rows a block moves at a time
+
+__global__ void __launch_bounds__(kCopyThreads) kv_move_kernel(const __grid_constant__ EvictArgs a, FastDiv chunks,
+                                                               int64_t rows, int pieces) {
+    __shared__ RowMove moves[kMoveRows];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t g = blockIdx.x; g < rows * pieces; g += gridDim.x) {
+        const int64_t row = g / pieces;
+        const int i0 = (int)(g - row * pieces) * kMoveRows;
+        const int b = (int)(row / a.src.heads), h = (int)(row - (int64_t)b * a.src.heads);
+        const int rn = min(kMoveRows, a.keep - i0);
+        if (threadIdx.x < rn) {
+            const int i = i0 + threadIdx.x;
+            const int32_t p = a.kept[row * a.keep + i];
+            RowMove mv{-1, 0, 0, 0};
+            int64_t sp, dp;
+            uint32_t ss, ds;
+            if (p >= 0 && locate(a.src, a.src.table + b * a.src.table_stride, (uint32_t)p, sp, ss) &&
+                locate(a.dst, a.dst.table + b * a.dst.table_stride, (uint32_t)i, dp, ds)) {
+                mv.k_from = sp * a.src.k_page_w + ss * a.src.k_slot_w + h * a.src.k_head_w;
+                mv.v_from = sp * a.src.v_page_w + ss * a.src.v_slot_w + h * a.src.v_head_w;
+                mv.k_to = dp * a.dst.k_page_w + ds * a.dst.k_slot_w + h * a.dst.k_head_w;
+                mv.v_to = dp * a.dst.v_page_w + ds * a.dst.v_slot_w + h * a.dst.v_head_w;
+            }
+            moves[threadIdx.x] = mv;
+        }
+        __syncthreads();
+        copy_rows<4>(moves, rn, chunks, a.src.k, a.src.v, a.dst.k, a.dst.v);
+        __syncthreads();
     }
 }
 
@@ -165,21 +402,90 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ Ev
 
 namespace dcp_host {
 
+namespace {
+
+dcp::FastDiv divisor(uint32_t d) {
+    dcp::FastDiv f;
+    const unsigned __int128 one = 1;
+    f.magic = d <= 1 ? 0 : (uint64_t)(((one << 64) + d - 1) / d);
+    f.d = d;
+    return f;
+}
+
+template <class T>
+T clamp(T v, T lo, T hi) {
+    return v < lo ? lo : v > hi ? hi : v;
+}
+
+bool vector_rows(const void *p, int64_t s0, int64_t s1) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && s0 % 4 == 0 && s1 % 4 == 0;
+}
+
+}  // namespace
+
 int32_t kv_append(const dcp::AppendArgs &a, cudaStream_t stream) {
-    const int64_t units = (int64_t)a.T * a.kv.heads;
-    dcp::kv_append_kernel<<<(unsigned)((units + 7) / 8), 256, 0, stream>>>(a);
+    // tokens per block: all of a block's rows at once, fewer where that would leave SMs without a block
+    const int64_t fit = clamp<int64_t>(dcp::kAppendRows / a.kv.heads, 1, 8);
+    const int64_t per = clamp<int64_t>(a.T / (2 * sm_count()), 1, fit);
+    const int64_t groups = (((int64_t)a.T - 1) / per + 1) * ((a.kv.heads - 1) / dcp::kAppendRows + 1);
+    const int64_t grid = groups < 16 * sm_count() ? groups : 16 * sm_count();
+    dcp::kv_append_kernel<<<(unsigned)grid, dcp::kCopyThreads, 0, stream>>>(a, (int)per, divisor(a.kv.data_w / 4));
     return launch_status("dcp_kv_append");
 }
 
 int32_t kv_weights(const dcp::WeightsArgs &a, cudaStream_t stream) {
-    dcp::kv_weights_kernel<<<(unsigned)(a.B * a.heads), 256, 0, stream>>>(a);
+    const int64_t rows = (int64_t)a.B * a.heads;
+    // blocks per row: one per 1024 positions, as long as that is not more than 16 waves
+    const int64_t stretches = ((int64_t)a.cap - 1) / (4 * dcp::kWeighThreads) + 1;
+    const int64_t splits = clamp<int64_t>(16 * 8 * sm_count() / rows, 1, stretches);
+    const bool vec = vector_rows(a.logits, a.logits_sb, a.logits_sh) && vector_rows(a.weights, a.w_sb, a.w_sh);
+    const int64_t grid = rows * splits;  // below 2^31: rows is, and splits is 1 where rows is large
+    if (vec)
+        dcp::kv_weights_kernel<true><<<(unsigned)grid, dcp::kWeighThreads, 0, stream>>>(a, (int)splits);
+    else
+        dcp::kv_weights_kernel<false><<<(unsigned)grid, dcp::kWeighThreads, 0, stream>>>(a, (int)splits);
     return launch_status("dcp_kv_weights");
 }
 
+template <int KPT>
+cudaError_t launch_select(const dcp::EvictArgs &a, int ctas, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.src.heads * ctas));
+    cfg.blockDim = dim3(dcp::kSelectThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ctas;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dcp::kv_select_kernel<KPT>, a);
+}
+
 int32_t kv_evict(const dcp::EvictArgs &a, cudaStream_t stream) {
-    const unsigned rows = (unsigned)a.B * (unsigned)a.src.heads;
-    dcp::kv_select_kernel<<<rows, 256, 0, stream>>>(a);
-    dcp::kv_move_kernel<<<dim3((unsigned)((a.keep + 7) / 8), rows), 256, 0, stream>>>(a);
+    const int64_t rows = (int64_t)a.B * a.src.heads;
+    // the longest row decides: 4 weights per thread of one CTA, else 16 and as many CTAs (at most
+    // 8, and at most what the grid's size allows) as hold it
+    const int64_t longest = a.cap < a.src.capacity ? a.cap : a.src.capacity;
+    int ctas = 1;
+    while (ctas < 8 && ctas * int64_t(16 * dcp::kSelectThreads) < longest && rows * ctas * 2 < (int64_t(1) << 31)) ctas *= 2;
+    const cudaError_t e = longest <= 4 * dcp::kSelectThreads ? launch_select<4>(a, 1, stream)
+                                                              : launch_select<16>(a, ctas, stream);
+    if (e != cudaSuccess) return launch_status("dcp_kv_evict");
+    const int pieces = (a.keep - 1) / dcp::kMoveRows + 1;
+    const int64_t blocks = rows * pieces;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(blocks < 32 * sm_count() ? blocks : 32 * sm_count()));
+    cfg.blockDim = dim3(dcp::kCopyThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, dcp::kv_move_kernel, a, divisor(a.src.data_w / 4), rows, pieces) != cudaSuccess)
+        return launch_status("dcp_kv_evict");
     return launch_status("dcp_kv_evict");
 }
 

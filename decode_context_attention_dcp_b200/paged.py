@@ -29,7 +29,7 @@ import math
 import torch
 
 # the package defines these before it imports this module
-from . import DCPError, _check, _code, _cuda, _stream, dcp_lse_pack_dim, library
+from . import DCPError, _code, _cuda, _stream, dcp_last_error, dcp_lse_pack_dim, library
 
 _i32, _i64, _ptr, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -71,17 +71,18 @@ def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tens
     if v_cache.dtype != k_cache.dtype:
         raise ValueError(f"{what}k_cache and v_cache differ in dtype")
     pages, page_size, heads, D = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if D > 1 and (ks[3] != 1 or vs[3] != 1):
+    kp, ks, kh, kd = k_cache.stride()
+    vp, vs, vh, vd = v_cache.stride()
+    if D > 1 and (kd != 1 or vd != 1):
         raise ValueError(f"{what}k_cache and v_cache must be contiguous in their last dimension")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != requests:
         raise ValueError(f"{what}block_table must be int32 [{requests}, max_pages], got {block_table.dtype} "
                          f"{tuple(block_table.shape)}")
-    width, ts = block_table.shape[1], block_table.stride()
-    if width > 1 and ts[1] != 1:
+    width, (tb, te) = block_table.shape[1], block_table.stride()
+    if width > 1 and te != 1:
         raise ValueError(f"{what}block_table must be contiguous in its last dimension")
-    return _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), pages, ks[0], ks[1], ks[2],
-                    vs[0], vs[1], vs[2], ts[0], width, page_size, heads, D, _code(k_cache.dtype))
+    return _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), pages, kp, ks, kh, vp, vs, vh, tb,
+                    width, page_size, heads, D, _code(k_cache.dtype))
 
 
 def _lens(seq_lens: torch.Tensor, requests: int) -> None:
@@ -103,12 +104,30 @@ def _rows(t: torch.Tensor, shape, what: str) -> tuple[int, int]:
 
 
 _workspace_bytes: dict = {}
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(device: torch.device, fn, *args) -> None:
+    """One library call with ``device`` current (a decode step makes several calls of a few
+    microseconds each, so the switch is made only where it is one)."""
+    if device.index == _current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status:
+        raise DCPError(status, dcp_last_error())
+
+
+def _raw_stream(device: torch.device, stream) -> int:
+    return _current_stream(device.index) if stream is None else _stream(device, stream)
 
 
 def paged_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor) -> int:
     """Bytes of workspace that attention of ``q`` [B, H, D] over ``k_cache`` needs on their device
     (whatever B and the lengths are)."""
-    key = (q.shape[1], k_cache.shape[2], k_cache.shape[3], k_cache.dtype, k_cache.device)
+    key = (q.shape[1], k_cache.shape[2], k_cache.shape[3], k_cache.dtype, k_cache.get_device())
     n = _workspace_bytes.get(key)
     if n is None:
         with torch.cuda.device(k_cache.device):
@@ -119,16 +138,17 @@ def paged_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor) -> int:
     return n
 
 
-def _scratch(nbytes: int, device: torch.device, stream) -> torch.Tensor | None:
+def _scratch(like: torch.Tensor, nbytes: int, stream) -> torch.Tensor | None:
     """Workspace for one call, in the order of the stream that the call runs on."""
     if nbytes == 0:
         return None
+    n = -(-nbytes // like.element_size())
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return like.new_empty(n)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return like.new_empty(n)
 
 
 def _attend(q, k_cache, v_cache, block_table, seq_lens, out, lse, world_size, scale, shard, num_shards, interleave,
@@ -137,29 +157,30 @@ def _attend(q, k_cache, v_cache, block_table, seq_lens, out, lse, world_size, sc
     B, H, D = q.shape
     kv = _cache(k_cache, v_cache, block_table, B)
     _lens(seq_lens, B)
-    if D != k_cache.shape[3] or q.dtype != k_cache.dtype:
+    if D != kv.head_dim or q.dtype != k_cache.dtype:
         raise ValueError(f"q {q.dtype} {tuple(q.shape)} does not match the cache {k_cache.dtype} "
                          f"{tuple(k_cache.shape)}")
-    qs = q.stride()
-    if D > 1 and qs[2] != 1:
+    qb, qh, qd = q.stride()
+    if D > 1 and qd != 1:
         raise ValueError("q must be contiguous in its last dimension")
-    ls = _rows(logits, (B, H, None), "logits") if logits is not None else (0, 0)
+    lg, lb, lh, cap = None, 0, 0, 0
+    if logits is not None:
+        lb, lh = _rows(logits, (B, H, None), "logits")
+        lg, cap = logits.data_ptr(), logits.shape[2]
     if scale is None:
         scale = 1.0 / math.sqrt(D) if D else 1.0
+    if workspace is None:
+        workspace = _scratch(q, paged_attention_workspace(q, k_cache), stream)
+    ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    tail = (qb, qh, lb, lh, cap, scale, shard, num_shards, interleave, 1 if is_lse_base_on_e else 0, ws, wsb,
+            _raw_stream(dev, stream))
     lib = library()
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = _scratch(paged_attention_workspace(q, k_cache), dev, stream)
-        tail = (ls[0], ls[1], logits.shape[2] if logits is not None else 0, scale, shard, num_shards, interleave,
-                1 if is_lse_base_on_e else 0, workspace.data_ptr() if workspace is not None else None,
-                workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(dev, stream))
-        lg = logits.data_ptr() if logits is not None else None
-        if world_size is None:
-            _check(lib.dcp_paged_attention(kv, q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), lg,
-                                           B, H, qs[0], qs[1], *tail))
-        else:
-            _check(lib.dcp_paged_attention_pack(kv, q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lg, B, H,
-                                                world_size, qs[0], qs[1], *tail))
+    if world_size is None:
+        _call(dev, lib.dcp_paged_attention, kv, q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), lg,
+              B, H, *tail)
+    else:
+        _call(dev, lib.dcp_paged_attention_pack, kv, q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lg, B, H,
+              world_size, *tail)
 
 
 def dcp_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -223,10 +244,9 @@ def dcp_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tenso
             or not query_start_loc.is_contiguous():
         raise ValueError(f"query_start_loc must be a contiguous int32 tensor of {R + 1} entries")
     ks, vs = k_new.stride(), v_new.stride()
-    with torch.cuda.device(dev):
-        _check(library().dcp_kv_append(kv, k_new.data_ptr(), v_new.data_ptr(), seq_lens.data_ptr(),
-                                       query_start_loc.data_ptr(), k_new.shape[0], R, ks[0], ks[1], vs[0], vs[1],
-                                       shard, num_shards, interleave, _stream(dev, stream)))
+    _call(dev, library().dcp_kv_append, kv, k_new.data_ptr(), v_new.data_ptr(), seq_lens.data_ptr(),
+          query_start_loc.data_ptr(), k_new.shape[0], R, ks[0], ks[1], vs[0], vs[1], shard, num_shards, interleave,
+          _raw_stream(dev, stream))
 
 
 def dcp_kv_weights(logits: torch.Tensor, global_lse: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Tensor,
@@ -245,10 +265,9 @@ def dcp_kv_weights(logits: torch.Tensor, global_lse: torch.Tensor, seq_lens: tor
     if global_lse.shape != (B, H) or global_lse.dtype != torch.float32:
         raise ValueError(f"global_lse must be fp32 [{B}, {H}], got {global_lse.dtype} {tuple(global_lse.shape)}")
     _lens(seq_lens, B)
-    with torch.cuda.device(dev):
-        _check(library().dcp_kv_weights(logits.data_ptr(), global_lse.data_ptr(), seq_lens.data_ptr(),
-                                        weights.data_ptr(), B, H, heads, cap, *ls, *global_lse.stride(), *ws, shard,
-                                        num_shards, interleave, 1 if is_lse_base_on_e else 0, _stream(dev, stream)))
+    _call(dev, library().dcp_kv_weights, logits.data_ptr(), global_lse.data_ptr(), seq_lens.data_ptr(),
+          weights.data_ptr(), B, H, heads, cap, *ls, *global_lse.stride(), *ws, shard, num_shards, interleave,
+          1 if is_lse_base_on_e else 0, _raw_stream(dev, stream))
 
 
 def dcp_kv_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -273,11 +292,9 @@ def dcp_kv_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         raise ValueError(f"kept must be a contiguous int32 [{B}, {heads}, {keep}] tensor")
     if tuple(new_lens.shape) != (B,) or new_lens.dtype != torch.int32 or not new_lens.is_contiguous():
         raise ValueError(f"new_lens must be a contiguous int32 [{B}] tensor")
-    with torch.cuda.device(dev):
-        _check(library().dcp_kv_evict(src, dst, seq_lens.data_ptr(), weights.data_ptr(), new_weights.data_ptr(),
-                                      kept.data_ptr(), new_lens.data_ptr(), B, weights.shape[2],
-                                      new_weights.shape[2], *ws, *ns, keep, recent, shard, num_shards, interleave,
-                                      _stream(dev, stream)))
+    _call(dev, library().dcp_kv_evict, src, dst, seq_lens.data_ptr(), weights.data_ptr(), new_weights.data_ptr(),
+          kept.data_ptr(), new_lens.data_ptr(), B, weights.shape[2], new_weights.shape[2], *ws, *ns, keep, recent,
+          shard, num_shards, interleave, _raw_stream(dev, stream))
 
 
 # ---- allocating helpers ------------------------------------------------------------------
@@ -286,8 +303,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     interleave: int = 1, logits: torch.Tensor | None = None, is_lse_base_on_e: bool = True):
     """Attention of q [B, H, D] over this rank's shard: (result [B, H, D], lse [B, H] fp32), the
     partial pair that pack() or lse_weighted_combine() takes.  See dcp_paged_attention."""
-    result = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    result = q.new_empty(q.shape)
+    lse = q.new_empty(q.shape[:2], dtype=torch.float32)
     dcp_paged_attention(q, k_cache, v_cache, block_table, seq_lens, result, lse, scale, shard, num_shards, interleave,
                         logits, is_lse_base_on_e)
     return result, lse
@@ -302,8 +319,7 @@ def paged_attention_pack(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     B, H, D = q.shape
     if world_size < 1 or H % world_size:
         raise ValueError(f"H={H} heads do not split over world_size={world_size}")
-    send = torch.empty((world_size, B, H // world_size, D + dcp_lse_pack_dim(q.dtype)), dtype=q.dtype,
-                       device=q.device)
+    send = q.new_empty((world_size, B, H // world_size, D + dcp_lse_pack_dim(q.dtype)))
     dcp_paged_attention_pack(q, k_cache, v_cache, block_table, seq_lens, send, world_size, scale, shard, num_shards,
                              interleave, logits, is_lse_base_on_e)
     return send
@@ -321,10 +337,9 @@ def kv_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
     B, heads, cap = weights.shape
-    dev = weights.device
-    kept = torch.empty((B, heads, keep), dtype=torch.int32, device=dev)
-    new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    new_weights = torch.empty((B, heads, max(cap, keep)), dtype=torch.float32, device=dev)
+    kept = weights.new_empty((B, heads, keep), dtype=torch.int32)
+    new_lens = weights.new_empty(B, dtype=torch.int32)
+    new_weights = weights.new_empty((B, heads, max(cap, keep)), dtype=torch.float32)
     dcp_kv_evict(weights, k_cache, v_cache, block_table, seq_lens, k_cache if k_out is None else k_out,
                  v_cache if v_out is None else v_out, new_block_table, keep, recent, kept, new_lens, new_weights,
                  shard, num_shards, interleave)
