@@ -22,6 +22,13 @@ struct FastDiv {
     __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)div_magic(n, magic); }
 };
 
+// n / d for n < 2^31: with 2^(s-1) < d <= 2^s and mul = ceil(2^(31+s) / d), the product exceeds
+// 2^(31+s) n / d by less than 2^(31+s) / d, so its quotient is exact; mul < 2^32.
+struct IntDiv {
+    uint32_t mul, shift, d;
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)(((uint64_t)n * mul) >> shift); }
+};
+
 struct PagedCache {
     uint32_t *k, *v;
     const int32_t *table;
@@ -32,7 +39,7 @@ struct PagedCache {
     int32_t capacity;  // max_pages * page_size: positions a table row can name
     int32_t heads;
     int32_t data_w;  // words per row, a multiple of 4
-    FastDiv page;    // page_size
+    IntDiv page;     // page_size
 };
 
 // The part of each request's positions that this rank holds.
@@ -79,7 +86,8 @@ struct AttentionArgs {
     float *partial;  // workspace
     int64_t q_sb_w, q_sh_w;
     int64_t logits_sb, logits_sh;
-    int32_t logits_cap;
+    int32_t logits_cap;   // 0: no logits
+    int32_t logits_pairs;  // rows start on 8 bytes
     int32_t B, H, group;  // group = H / kv.heads
     int32_t row_blocks, head_blocks;  // passes per group (set at launch), and over all key heads
     int32_t pack_hr;      // heads per rank of the packed send buffer, 0 = plain result

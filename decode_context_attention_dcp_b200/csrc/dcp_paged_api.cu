@@ -26,6 +26,16 @@ dcp::FastDiv fast_div(uint64_t d) {
     return f;
 }
 
+dcp::IntDiv int_div(uint32_t d) {
+    dcp::IntDiv f;
+    uint32_t s = 0;
+    while ((uint64_t(1) << s) < d) ++s;
+    f.mul = (uint32_t)(((uint64_t(1) << (31 + s)) + d - 1) / d);
+    f.shift = 31 + s;
+    f.d = d;
+    return f;
+}
+
 int64_t attention_workspace(int32_t group, int32_t head_dim, int32_t dtype) {
     switch (dtype) {
         case DCP_BF16: return dcp_host::attention_workspace_bf16(group, head_dim);
@@ -74,7 +84,7 @@ int32_t check_cache(const char *fn, const dcp_paged_kv *kv, bool used, dcp::Page
     c.capacity = (int32_t)(kv->max_pages * kv->page_size);
     c.heads = kv->heads;
     c.data_w = kv->head_dim * es / 4;
-    c.page = fast_div((uint64_t)kv->page_size);
+    c.page = int_div((uint32_t)kv->page_size);
     return DCP_OK;
 }
 
@@ -152,6 +162,7 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
     a.logits_sb = logits_stride_b;
     a.logits_sh = logits_stride_h;
     a.logits_cap = logits ? (int32_t)logits_cap : 0;
+    a.logits_pairs = aligned(logits, 8) && logits_stride_b % 2 == 0 && logits_stride_h % 2 == 0;
     a.B = (int32_t)B;
     a.H = (int32_t)H;
     a.group = (int32_t)(H / kv->heads);

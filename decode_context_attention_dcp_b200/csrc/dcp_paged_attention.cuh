@@ -71,18 +71,21 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
+}
+
 // 16 bytes global -> shared, or 16 zero bytes (nothing read).
 __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, bool read) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16u : 0u));
 }
 
-// A float as two tf32 values, hi + lo = x to 2^-22 |x|: hi is x rounded to 10 fraction bits (half
-// a step away from zero), lo the rest, rounded alike.
-__device__ __forceinline__ uint32_t tf32_round(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
-
+// A float as two tf32 values: hi is x rounded to 10 fraction bits (half a step away from zero), lo
+// the rest (at most 2^-11 |x|), of which the product keeps 10 fraction bits: hi + lo = x to
+// 2^-21 |x|.
 __device__ __forceinline__ void tf32_split(float x, uint32_t &hi, uint32_t &lo) {
-    hi = tf32_round(x);
-    lo = tf32_round(x - __uint_as_float(hi));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
 // ---- shapes -----------------------------------------------------------------------------------
@@ -102,22 +105,27 @@ struct AttentionShape {
     static constexpr int kHalf = WP * DP * kBytes;     // bytes of a stage's K (and of its V)
     static constexpr int kStage = 2 * kHalf;           // = 64 DP: also 16 fp32 rows of DP
     static constexpr int kQuery = kRows * DP * kBytes;  // bytes of one query buffer
+    static constexpr int kQueries = kHalfType ? ST * kQuery : 2 * kQuery;  // one per stage; fp32: one, as pairs
     static constexpr int kThreads = NW * 32;
     static constexpr bool kQueryRegs = kHalfType && MT * DP <= 128;
-    static constexpr size_t kSmem = (size_t)NW * ST * kStage + (size_t)ST * kQuery;
+    static constexpr size_t kSmem = (size_t)NW * ST * kStage + kQueries;
     static_assert(kStage == 16 * DP * 4, "a stage holds one block of fp32 rows");
 };
 
-// Weights are carried as 2^(x - m + kShift): the two fp16 parts of a weight then keep their 11 + 11
-// bits down to weights of 2^-29, where those below 2^-14 would otherwise be subnormal.  The
-// largest, 2^15, stays below the fp16 maximum.  The factor cancels in the division by the sum.
+// How far a logit (base 2) may exceed the running maximum before the sums are rescaled.
+constexpr float kSlack = 7.f;
+
+// Weights are carried as 2^(x - m + shift): the two fp16 parts of a weight then keep their 11 + 11
+// bits down to weights of 2^-22, where those below 2^-14 would otherwise be subnormal.  The
+// largest, 2^(8 + kSlack), stays below the fp16 maximum.  The factor cancels in the division by the
+// sum.
 template <class T>
 struct WeightShift {
     static constexpr float value = 0.f;
 };
 template <>
 struct WeightShift<Fp16> {
-    static constexpr float value = 15.f;
+    static constexpr float value = 8.f;
 };
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -127,7 +135,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // Two partials per CTA (the request it entered in the middle, the one it left unfinished): kRows
 // rows of DP floats each, then (maximum, sum) per row, then one int4 per CTA: the number of
 // parts of the request that starts in this CTA and is finished by later ones (0: none), its
-// request and head block.
+// request, key head and row block.
 struct Workspace {
     float *rows;
     float2 *stats;
@@ -169,10 +177,10 @@ struct Shares {
     }
 };
 
-// Position in the sequence of tiles: request b, head block hb (key head and row block), tile t of
-// nt; n is the request's local length.  The next request's length is read one request ahead.
+// Position in the sequence of tiles: tile t of nt of request b, key head kvh and row block rb; n
+// is the request's local length.  The next request's length is read one request ahead.
 struct TileIter {
-    int b, hb, t, n, nt, next_seq;
+    int b, kvh, rb, t, n, nt, next_seq;
 };
 
 __device__ __forceinline__ int tiles_of(int n, int tile) { return n > tile ? (n - 1) / tile + 1 : 1; }
@@ -188,8 +196,10 @@ template <int TILE>
 __device__ __forceinline__ void iter_next(const AttentionArgs &a, TileIter &it) {
     if (++it.t < it.nt) return;
     it.t = 0;
-    if (++it.hb < a.head_blocks) return;
-    it.hb = 0;
+    if (++it.rb < a.row_blocks) return;
+    it.rb = 0;
+    if (++it.kvh < a.kv.heads) return;
+    it.kvh = 0;
     ++it.b;
     iter_request<TILE>(a, it);
 }
@@ -250,7 +260,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     __shared__ int s_where[4];
     __shared__ float2 s_stat[NW][S::kRows];        // maximum and sum of each warp's rows at a merge
     __shared__ uint32_t s_held[ST][NW];            // bit r: position r of the warp's stage counts
-    __shared__ longlong2 s_off[NW][WP];            // word offsets of the rows being copied
+    __shared__ longlong2 s_row[NW][WP];            // addresses of the K and V rows being copied
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");
 
@@ -302,32 +312,47 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     }
     TileIter ld;
     ld.b = s_where[0];
-    ld.hb = s_where[1];
+    ld.kvh = s_where[1] / a.row_blocks;
+    ld.rb = s_where[1] - ld.kvh * a.row_blocks;
     ld.t = s_where[2];
     ld.next_seq = a.seq_lens[ld.b];
     iter_request<TILE>(a, ld);
     TileIter cp = ld;
 
     const uint32_t stages = smem_addr(smem) + warp * (ST * S::kStage);
-    uint8_t *const stages_p = smem;
     const uint32_t queries = smem_addr(smem) + NW * ST * S::kStage;
+    uint2 *const query_pairs = reinterpret_cast<uint2 *>(smem + NW * ST * S::kStage);  // fp32
 
-    // The page of this lane's position of the tile that is copied next is read one tile ahead.
-    auto page_entry = [&](const TileIter &it) -> int {
-        const int p = it.t * TILE + warp * WP + (lane & (WP - 1));
-        return p < it.n ? __ldg(a.kv.table + it.b * a.kv.table_stride + a.kv.page.div((uint32_t)p)) : -1;
+    // This lane's row of the tile that is copied next: its page is read one tile ahead.
+    int entry = -1;
+    uint32_t slot = 0;
+    auto next_page = [&]() {
+        const int p = ld.t * TILE + warp * WP + (lane & (WP - 1));
+        entry = -1;
+        if (p < ld.n) {
+            const uint32_t j = a.kv.page.div((uint32_t)p);
+            slot = (uint32_t)p - j * a.kv.page.d;
+            entry = __ldg(a.kv.table + ld.b * a.kv.table_stride + j);
+        }
     };
-    int entry = page_entry(ld);
+    next_page();
     int ld_query = 0, ld_stage = 0;
+
+    // One warp-wide copy covers kRowsPerCopy rows (or a 32-chunk part of one).  Chunk c of row r lies
+    // at chunk c ^ (r mod 8) of its row in shared memory, so that the 8 rows of an ldmatrix, or
+    // of a fragment's float reads, fall into different banks.
+    constexpr int kRowsPerCopy = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;  // rows per warp-wide copy
+    constexpr int kCopiesPerRow = S::kChunks > 32 ? S::kChunks / 32 : 1;
+    const int my_row = S::kChunks > 32 ? 0 : lane / S::kChunks, my_chunk = S::kChunks > 32 ? lane : lane % S::kChunks;
+    const uint32_t lane_to = my_row * S::kChunks * 16, lane_sw = (uint32_t)(my_chunk ^ my_row) << 4;
 
     // Starts the copies of the next tile (this warp's positions of it; the query with a new
     // request or head block) and moves on.
     auto copy_next = [&](bool first) {
-        const int kvh = a.row_blocks == 1 ? ld.hb : ld.hb / a.row_blocks;
-        if (first || ld.t == 0) {
-            const int row0 = (ld.hb - kvh * a.row_blocks) * S::kRows;
+        if (S::kHalfType && (first || ld.t == 0)) {
+            const int row0 = ld.rb * S::kRows;
             const uint32_t dst = queries + ld_query * S::kQuery;
-            const uint32_t *src = a.q + ld.b * a.q_sb_w + (int64_t)(kvh * a.group + row0) * a.q_sh_w;
+            const uint32_t *src = a.q + ld.b * a.q_sb_w + (int64_t)(ld.kvh * a.group + row0) * a.q_sh_w;
             for (int i = tid; i < S::kRows * S::kChunks; i += S::kThreads) {
                 const int r = i / S::kChunks, c = i - r * S::kChunks;
                 const bool in = row0 + r < a.group && c * 4 < a.kv.data_w;
@@ -335,35 +360,43 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
             }
             ld_query = ld_query + 1 == ST ? 0 : ld_query + 1;
         }
-        const int p0 = ld.t * TILE + warp * WP;
-        if (p0 < ld.n) {
-            const int r = lane & (WP - 1), p = p0 + r;
-            const bool held = p < ld.n && entry >= 0 && entry < a.kv.num_pages;
-            const uint32_t slot = (uint32_t)p - a.kv.page.div((uint32_t)p) * a.kv.page.d;
-            __syncwarp();  // the last tile's offsets have been read
+        if (ld.t * TILE + warp * WP < ld.n) {
+            const bool held = entry >= 0 && entry < a.kv.num_pages;
+            __syncwarp();  // the last tile's addresses have been read
             if (lane < WP) {
-                longlong2 off;
-                off.x = held ? entry * a.kv.k_page_w + slot * a.kv.k_slot_w + kvh * a.kv.k_head_w : -1;
-                off.y = entry * a.kv.v_page_w + slot * a.kv.v_slot_w + kvh * a.kv.v_head_w;
-                s_off[warp][r] = off;
+                longlong2 at;  // byte addresses of the rows' first chunks
+                at.x = reinterpret_cast<int64_t>(a.kv.k) +
+                       4 * (entry * a.kv.k_page_w + slot * a.kv.k_slot_w + ld.kvh * a.kv.k_head_w);
+                at.y = reinterpret_cast<int64_t>(a.kv.v) +
+                       4 * (entry * a.kv.v_page_w + slot * a.kv.v_slot_w + ld.kvh * a.kv.v_head_w);
+                s_row[warp][lane] = at;
             }
-            const uint32_t bits = __ballot_sync(0xffffffffu, held);
-            if (lane == 0) s_held[ld_stage][warp] = WP == 32 ? bits : bits & ((1u << WP) - 1u);
+            const uint32_t bits = __ballot_sync(0xffffffffu, held) & ((1u << WP) - 1u);
+            if (lane == 0) s_held[ld_stage][warp] = bits;
             __syncwarp();
-            const uint32_t dst = stages + ld_stage * S::kStage;
+            const uint32_t dst = stages + ld_stage * S::kStage + lane_to;
+            const bool all = bits == (1u << WP) - 1u && S::DP * S::kBytes == 4 * a.kv.data_w;
 #pragma unroll
             for (int i = 0; i < WP * S::kChunks / 32; ++i) {
-                const int x = i * 32 + lane, row = x / S::kChunks, c = x - row * S::kChunks;
-                const longlong2 off = s_off[warp][row];
-                const bool in = off.x >= 0 && c * 4 < a.kv.data_w;
-                const uint32_t to = dst + (row * S::kChunks + (c ^ (row & 7))) * 16;
-                cp_async_or_zero(to, in ? a.kv.k + off.x + c * 4 : a.kv.k, in);
-                cp_async_or_zero(to + S::kHalf, in ? a.kv.v + off.y + c * 4 : a.kv.v, in);
+                const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
+                const longlong2 at = s_row[warp][row0 + my_row];
+                // row0 + my_row mod 8 = (row0 mod 8) ^ my_row: my_row < kRowsPerCopy, which divides row0
+                const uint32_t to = dst + ((lane_sw ^ ((row0 & 7) << 4)) + (row0 * S::kChunks + c0) * 16);
+                const char *k = reinterpret_cast<const char *>(at.x) + (my_chunk + c0) * 16;
+                const char *v = reinterpret_cast<const char *>(at.y) + (my_chunk + c0) * 16;
+                if (all) {
+                    cp_async_16(to, k);
+                    cp_async_16(to + S::kHalf, v);
+                } else {
+                    const bool in = ((bits >> (row0 + my_row)) & 1u) && (my_chunk + c0) * 4 < a.kv.data_w;
+                    cp_async_or_zero(to, in ? (const void *)k : a.kv.k, in);
+                    cp_async_or_zero(to + S::kHalf, in ? (const void *)v : a.kv.v, in);
+                }
             }
         }
         ld_stage = ld_stage + 1 == ST ? 0 : ld_stage + 1;
         iter_next<TILE>(a, ld);
-        entry = page_entry(ld);
+        next_page();
     };
 
     for (int i = 0; i < ST - 1; ++i) {
@@ -373,28 +406,55 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
 
     const float scale2 = a.scale * kLog2e;
     const int g = lane >> 2, t4 = lane & 3;
+    const bool upper = a.group > 8;  // rows 8..15 of a block hold query heads
     float o[MT][DP / 8][4], m[MT][2], sum[MT][2];
     uint32_t qf[S::kQueryRegs ? MT : 1][S::kQueryRegs ? DP / 16 : 1][4];
     int cp_query = 0, cp_stage = 0, first_t = cp.t;
     uint32_t query = queries;
+    // ldmatrix places of this lane: K rows for the first product, V rows (transposed) for the second.
+    // Chunk 2 j + e of row r lies at ((2 j + e) ^ (r mod 8)): 16-byte steps that depend on j mod 4
+    // through these, the rest is a constant 128 (j / 4).
+    uint32_t k_at[4], v_at[4];
+    {
+        const int rk = (lane & 7) + ((lane >> 4) << 3), rv = lane & 15;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            k_at[j] = rk * (DP * 2) + (((2 * j + ((lane >> 3) & 1)) ^ (rk & 7)) << 4);
+            v_at[j] = S::kHalf + rv * (DP * 2) + (((2 * j + (lane >> 4)) ^ (rv & 7)) << 4);
+        }
+    }
 
     for (int64_t i = 0; i < count; ++i) {
         if (i + ST - 1 < count) copy_next(false);
         cp_async_commit();
         cp_async_wait<ST - 1>();
-        if (i == 0 || cp.t == 0) {  // a new request or head block: every warp's part of the query has arrived
-            __syncthreads();
-            query = queries + cp_query * S::kQuery;
-            cp_query = cp_query + 1 == ST ? 0 : cp_query + 1;
+        if (i == 0 || cp.t == 0) {  // a new request or head block
             first_t = cp.t;
-            if constexpr (S::kQueryRegs) {
+            if constexpr (S::kHalfType) {
+                __syncthreads();  // every warp's part of the query has arrived
+                query = queries + cp_query * S::kQuery;
+                cp_query = cp_query + 1 == ST ? 0 : cp_query + 1;
+                if constexpr (S::kQueryRegs) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        const int r = mt * 16 + (lane & 15), c = 2 * ks + (lane >> 4);
-                        ldmatrix4(qf[mt][ks], query + (r * S::kChunks + (c ^ (r & 7))) * 16);
-                    }
+                        for (int ks = 0; ks < DP / 16; ++ks) {
+                            const int r = mt * 16 + (lane & 15), c = 2 * ks + (lane >> 4);
+                            ldmatrix4(qf[mt][ks], query + (r * S::kChunks + (c ^ (r & 7))) * 16);
+                        }
+                }
+            } else {
+                // the query as (hi, lo) pairs, split once: row r, element d at r * DP + (d ^ 4 (r mod 8))
+                const int row0 = cp.rb * S::kRows;
+                const uint32_t *src = a.q + cp.b * a.q_sb_w + (int64_t)(cp.kvh * a.group + row0) * a.q_sh_w;
+                for (int x = tid; x < S::kRows * DP; x += S::kThreads) {
+                    const int r = x / DP, d = x - r * DP;
+                    const bool in = row0 + r < a.group && d < a.kv.data_w;
+                    uint2 pair;
+                    tf32_split(in ? __uint_as_float(src[r * a.q_sh_w + d]) : 0.f, pair.x, pair.y);
+                    query_pairs[r * DP + (d ^ ((r & 7) << 2))] = pair;
+                }
+                __syncthreads();
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -409,7 +469,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         const int p0 = cp.t * TILE + warp * WP;
         if (p0 < cp.n) {
             constexpr int NT = WP / 8;  // 8-position blocks of the product
-            const uint32_t kt = stages + cp_stage * S::kStage, vt = kt + S::kHalf;
+            const uint32_t stage = stages + cp_stage * S::kStage;
             const uint32_t held = s_held[cp_stage][warp];
             float x[MT][NT][4];
             // ---- x = q . k
@@ -418,12 +478,10 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[mt][0][e] = x[mt][NT - 1][e] = 0.f;
-                const int r = (lane & 7) + ((lane >> 4) << 3);
-                const uint32_t row = kt + r * (DP * 2), sw = (((lane >> 3) & 1) ^ (r & 7)) << 4;
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
                     uint32_t kb[4];
-                    ldmatrix4(kb, row + ((ks * 32) ^ sw));
+                    ldmatrix4(kb, stage + k_at[ks & 3] + (ks >> 2) * 128);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         uint32_t qa[4];
@@ -443,18 +501,17 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                 float x1[4] = {0.f, 0.f, 0.f, 0.f}, x2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[0][0][e] = 0.f;
-                const float *kr = reinterpret_cast<const float *>(stages_p + (kt - smem_addr(smem))) + g * DP + t4;
-                const float *qr = reinterpret_cast<const float *>(stages_p + (query - smem_addr(smem))) + g * DP + t4;
-#pragma unroll 4
+                const float *kr = reinterpret_cast<const float *>(smem + (stage - smem_addr(smem))) + g * DP + t4;
+                const uint2 *qr = query_pairs + g * DP + t4;
+#pragma unroll
                 for (int ks = 0; ks < DP / 8; ++ks) {
                     const int c0 = ((2 * ks) ^ g) * 4, c1 = ((2 * ks + 1) ^ g) * 4;
-                    uint32_t kh[2], kl[2], qh[4], ql[4];
+                    uint32_t kh[2], kl[2];
                     tf32_split(kr[c0], kh[0], kl[0]);
                     tf32_split(kr[c1], kh[1], kl[1]);
-                    tf32_split(qr[c0], qh[0], ql[0]);
-                    tf32_split(qr[8 * DP + c0], qh[1], ql[1]);
-                    tf32_split(qr[c1], qh[2], ql[2]);
-                    tf32_split(qr[8 * DP + c1], qh[3], ql[3]);
+                    const uint2 q0 = qr[c0], q1 = upper ? qr[8 * DP + c0] : make_uint2(0u, 0u), q2 = qr[c1],
+                                q3 = upper ? qr[8 * DP + c1] : make_uint2(0u, 0u);
+                    const uint32_t qh[4] = {q0.x, q1.x, q2.x, q3.x}, ql[4] = {q0.y, q1.y, q2.y, q3.y};
                     mma(T{}, x[0][0], qh, kh[0], kh[1]);
                     mma(T{}, x1, qh, kl[0], kl[1]);
                     mma(T{}, x2, ql, kh[0], kh[1]);
@@ -462,7 +519,37 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[0][0][e] += x1[e] + x2[e];
             }
-            // ---- logits, mask
+            // ---- logits
+            if (a.logits_cap) {
+                const int row0 = cp.rb * S::kRows, end = min(cp.n, a.logits_cap);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int r = row0 + mt * 16 + half * 8 + g;
+                        if (r >= a.group) continue;
+                        float *to = a.logits + cp.b * a.logits_sb + (int64_t)(cp.kvh * a.group + r) * a.logits_sh + p0;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int c = nt * 8 + 2 * t4;
+                            const float v0 = (held >> c) & 1u ? x[mt][nt][2 * half] * a.scale : -INFINITY;
+                            const float v1 = (held >> (c + 1)) & 1u ? x[mt][nt][2 * half + 1] * a.scale : -INFINITY;
+                            if (a.logits_pairs && p0 + WP <= end) {
+                                *reinterpret_cast<float2 *>(to + c) = make_float2(v0, v1);
+                            } else {
+                                if (p0 + c < end) to[c] = v0;
+                                if (p0 + c + 1 < end) to[c + 1] = v1;
+                            }
+                        }
+                    }
+            }
+            // ---- base-2 logits, masked
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[mt][nt][e] *= scale2;
             if (held != (1u << WP) - 1u) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -472,61 +559,41 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                         for (int e = 0; e < 4; ++e)
                             if (!((held >> (nt * 8 + 2 * t4 + (e & 1))) & 1u)) x[mt][nt][e] = -INFINITY;
             }
-            if (a.logits_cap) {
-                const int kvh = a.row_blocks == 1 ? cp.hb : cp.hb / a.row_blocks;
-                const int row0 = (cp.hb - kvh * a.row_blocks) * S::kRows, end = min(cp.n, a.logits_cap);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int r = row0 + mt * 16 + half * 8 + g;
-                        if (r >= a.group) continue;
-                        float *to = a.logits + cp.b * a.logits_sb + (int64_t)(kvh * a.group + r) * a.logits_sh;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const int p = p0 + nt * 8 + 2 * t4;
-                            // a masked x stays -inf whatever the scale
-                            const float v0 = x[mt][nt][2 * half], v1 = x[mt][nt][2 * half + 1];
-                            const bool h0 = (held >> (nt * 8 + 2 * t4)) & 1u, h1 = (held >> (nt * 8 + 2 * t4 + 1)) & 1u;
-                            if (p < end) to[p] = h0 ? v0 * a.scale : -INFINITY;
-                            if (p + 1 < end) to[p + 1] = h1 ? v1 * a.scale : -INFINITY;
-                        }
-                    }
-            }
-            // ---- running maximum, weights
+            // ---- running maximum and weights.  The maximum m moves only when a logit exceeds it by more
+            // than kSlack: weights up to 2^kSlack are as exact, and the rescale is nearly never needed.
             bool grew = false;
             float keep[MT][2];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    float top = -INFINITY;
+                    keep[mt][half] = 1.f;
+                    if (half == 1 && !upper) {  // no query heads there: zero weights
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float &v = x[mt][nt][2 * half + e];
-                            const int col = nt * 8 + 2 * t4 + e;
-                            v = ((held >> col) & 1u) ? v * scale2 : -INFINITY;
-                            top = fmaxf(top, v);
-                        }
+                        for (int nt = 0; nt < NT; ++nt) x[mt][nt][2] = x[mt][nt][3] = 0.f;
+                        continue;
+                    }
+                    float top = fmaxf(x[mt][0][2 * half], x[mt][0][2 * half + 1]);
+                    if (NT == 2) top = fmaxf(top, fmaxf(x[mt][NT - 1][2 * half], x[mt][NT - 1][2 * half + 1]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float old = m[mt][half], now = fmaxf(old, top);
-                    grew |= now > old;
-                    m[mt][half] = now;
-                    const float base = finite_or_zero_max(now);
-                    keep[mt][half] = exp2_fast(old - base);
+                    const float old = m[mt][half];
+                    if (top > old + kSlack) {
+                        grew = true;
+                        m[mt][half] = top;
+                        keep[mt][half] = exp2_fast(old - top);
+                    }
+                    const float base = finite_or_zero_max(m[mt][half]) - WeightShift<T>::value;
                     float add = 0.f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float &v = x[mt][nt][2 * half + e];
-                            v = exp2_fast(v - (base - WeightShift<T>::value));
+                            v = exp2_fast(v - base);
                             add += v;
                         }
-                    sum[mt][half] = fmaf(sum[mt][half], old == now ? 1.f : keep[mt][half], add);
+                    sum[mt][half] = fmaf(sum[mt][half], keep[mt][half], add);
                 }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -554,12 +621,10 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                         rest[1] = w[1] - back[1];
                         lo[mt][f] = T::encode(rest);
                     }
-                const int r = lane & 15;
-                const uint32_t row = vt + r * (DP * 2), sw = ((lane >> 4) ^ (r & 7)) << 4;
 #pragma unroll
                 for (int j = 0; j < DP / 16; ++j) {
                     uint32_t vb[4];
-                    ldmatrix4_trans(vb, row + ((j * 32) ^ sw));
+                    ldmatrix4_trans(vb, stage + v_at[j & 3] + (j >> 2) * 128);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         mma(T{}, o[mt][2 * j], hi[mt], vb[0], vb[1]);
@@ -576,7 +641,8 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                 tf32_split(x[0][0][2], wh[1], wl[1]);
                 tf32_split(x[0][0][1], wh[2], wl[2]);
                 tf32_split(x[0][0][3], wh[3], wl[3]);
-                const float *v0 = reinterpret_cast<const float *>(stages_p + (vt - smem_addr(smem))) + (2 * t4) * DP + (g & 3);
+                const float *v0 = reinterpret_cast<const float *>(smem + (stage + S::kHalf - smem_addr(smem))) +
+                                  (2 * t4) * DP + (g & 3);
 #pragma unroll
                 for (int j = 0; j < DP / 8; ++j) {
                     const int c = 2 * j + (g >> 2);
@@ -594,8 +660,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         // ---- the end of a request, or of the share: merge the warps
         const bool last = cp.t + 1 == cp.nt;
         if (last || i + 1 == count) {
-            const int kvh = a.row_blocks == 1 ? cp.hb : cp.hb / a.row_blocks;
-            const int row0 = (cp.hb - kvh * a.row_blocks) * S::kRows;
+            const int kvh = cp.kvh, row0 = cp.rb * S::kRows;
             const bool whole = last && first_t == 0;
             const Workspace ws = workspace_at<S::kRows, DP>(a.partial, gridDim.x);
             const int64_t slot = 2 * (int64_t)blockIdx.x + (first_t == 0 ? 1 : 0);
@@ -609,7 +674,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                     if (t4 == 0) s_stat[warp][mt * 16 + half * 8 + g] = make_float2(m[mt][half], s);
                 }
                 // this tile's stage is free until the next copy_next: 16 fp32 rows
-                uint8_t *mine = stages_p + (size_t)(warp * ST + cp_stage) * S::kStage;
+                uint8_t *mine = smem + (size_t)(warp * ST + cp_stage) * S::kStage;
 #pragma unroll
                 for (int j = 0; j < DP / 8; ++j)
 #pragma unroll
@@ -636,7 +701,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                     for (int w = 0; w < NW; ++w) {
                         const float f = exp2_fast(st[w].x - base);
                         const float4 v = *reinterpret_cast<const float4 *>(
-                            stages_p + (size_t)(w * ST + cp_stage) * S::kStage + r * (DP * 4) + ((c ^ (r & 7)) << 4));
+                            smem + (size_t)(w * ST + cp_stage) * S::kStage + r * (DP * 4) + ((c ^ (r & 7)) << 4));
                         total = fmaf(st[w].y, f, total);
                         acc.x = fmaf(v.x, f, acc.x);
                         acc.y = fmaf(v.y, f, acc.y);
@@ -654,7 +719,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                 __syncthreads();
             }
             if (i + 1 == count && tid == 0) {
-                int4 spill = make_int4(0, cp.b, cp.hb, 0);
+                int4 spill = make_int4(0, cp.b, kvh, cp.rb);
                 // parts: this share and those up to the one with the request's last tile
                 if (first_t == 0 && !last)
                     spill.x = (int)(shares.of(begin + i + (cp.nt - 1 - cp.t)) - blockIdx.x) + 1;
@@ -677,7 +742,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
     const int4 spill = ws.spill[blockIdx.x];
     const int parts = spill.x, r = blockIdx.y, lane = threadIdx.x & 31;
     if (parts == 0) return;
-    const int kvh = spill.z / a.row_blocks, row = (spill.z - kvh * a.row_blocks) * ROWS + r;
+    const int kvh = spill.z, row = spill.w * ROWS + r;
     if (row >= a.group) return;
     // part 0 is the share's unfinished request, the others the requests entered in the middle
     auto slot = [&](int p) { return (int64_t)(2 * ((int64_t)blockIdx.x + p) + (p == 0 ? 1 : 0)) * ROWS + r; };
