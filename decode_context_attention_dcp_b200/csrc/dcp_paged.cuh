@@ -87,7 +87,6 @@ struct AttentionArgs {
     int64_t q_sb_w, q_sh_w;
     int64_t logits_sb, logits_sh;
     int32_t logits_cap;   // 0: no logits
-    int32_t logits_pairs;  // rows start on 8 bytes
     int32_t B, H, group;  // group = H / kv.heads
     int32_t row_blocks, head_blocks;  // passes per group (set at launch), and over all key heads
     int32_t pack_hr;      // heads per rank of the packed send buffer, 0 = plain result

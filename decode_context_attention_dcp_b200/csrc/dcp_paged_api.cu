@@ -162,7 +162,6 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
     a.logits_sb = logits_stride_b;
     a.logits_sh = logits_stride_h;
     a.logits_cap = logits ? (int32_t)logits_cap : 0;
-    a.logits_pairs = aligned(logits, 8) && logits_stride_b % 2 == 0 && logits_stride_h % 2 == 0;
     a.B = (int32_t)B;
     a.H = (int32_t)H;
     a.group = (int32_t)(H / kv->heads);

@@ -6,20 +6,21 @@
 // What bounds it.  A position costs 2 D elements of K and V per key head and 4 G D flops for the G
 // query heads that share it: G flops per byte (16-bit), far below the machine's balance for any
 // group of this size, so the kernel is a stream over the held pages and everything else is
-// arranged to keep that stream full.  The products are small (G rows); they run on
-// mma.sync (m16n8k16, fp32 sums), whose operands come straight from the streamed tile.  tcgen05
-// would want 128 rows per product and an operand round trip through tensor memory, for a pipe
-// that is idle most of the time either way.
+// arranged to keep that stream full.  The products run on mma.sync (m16n8k16, fp32 sums) with
+// positions (x = K q^T) and then columns (o^T = V^T p^T) as the 16 rows and query heads as the 8 columns, so
+// that a group of up to 8 heads costs one product per 16 x 16 block of K or V.  Operands come
+// straight from the streamed tile.  tcgen05 would want 128 rows per product and an operand round
+// trip through tensor memory, for a pipe that is idle most of the time either way.
 //
-// Work split.  The tiles (TILE positions of one request, key head and block of query rows) of the whole batch
-// are numbered in a row and divided evenly over the CTAs of one resident wave, whatever the
-// lengths: a CTA's share may begin and end inside a request.  Each CTA finds its share from the
-// lengths on the device.  A request that lies in one share is finished there; the others leave
-// one fp32 partial (unnormalised row, maximum, sum) per share in the workspace, and attention_join_kernel
-// merges them in share order (no atomics: the same bits every time).
+// Work split.  The tiles (TILE positions of one request, key head and block of query heads) of the
+// whole batch are numbered in a row and divided evenly over the CTAs of one resident wave, whatever
+// the lengths: a CTA's share may begin and end inside a request.  Each CTA finds its share from
+// the lengths on the device.  A request that lies in one share is finished there; the others leave
+// one fp32 partial (unnormalised row, maximum, sum) per share in the workspace, and
+// attention_join_kernel merges them in share order (no atomics: the same bits every time).
 //
 // Inside a CTA each warp streams its own positions (warp w of NW takes every NW-th group of
-// WP) through its own ring of shared-memory stages with cp.async, and keeps its own softmax
+// 16) through its own ring of shared-memory stages with cp.async, and keeps its own softmax
 // state; warps meet only where a request begins (the query) and ends (the merge).
 #pragma once
 
@@ -38,6 +39,13 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t *r, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
+}
+
+// The transpose of an 8 x 8 block of 16-bit elements spread over the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 __device__ __forceinline__ void mma(Bf16, float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
@@ -89,27 +97,27 @@ __device__ __forceinline__ void tf32_split(float x, uint32_t &hi, uint32_t &lo) 
 }
 
 // ---- shapes -----------------------------------------------------------------------------------
-// T element type, DP head dim as laid out in shared memory (D <= DP, the rest zero), MT 16-row
-// blocks of query heads per pass over K and V, NW warps per CTA, ST stages per warp, CTAS resident
-// CTAs per SM.
-template <class T_, int DP_, int MT_, int NW_, int ST_, int CTAS_>
+// T element type, DP head dim as laid out in shared memory (D <= DP, the rest zero), NH blocks of 8
+// query heads per pass over K and V, NW warps per CTA, ST stages per warp, CTAS resident CTAs per SM.
+template <class T_, int DP_, int NH_, int NW_, int ST_, int CTAS_>
 struct AttentionShape {
     using T = T_;
-    static constexpr int DP = DP_, MT = MT_, NW = NW_, ST = ST_, CTAS = CTAS_;
+    static constexpr int DP = DP_, NH = NH_, NW = NW_, ST = ST_, CTAS = CTAS_;
     static constexpr bool kHalfType = T::kPerWord == 2;
     static constexpr int kBytes = 4 / T::kPerWord;     // element size
-    static constexpr int WP = kHalfType ? 16 : 8;      // positions per warp and stage: one k step of P V
+    static constexpr int WP = 16;                      // positions per warp and stage
     static constexpr int TILE = WP * NW;               // positions per CTA tile
-    static constexpr int kRows = 16 * MT;              // query rows per pass
+    static constexpr int kHeads = 8 * NH;              // query heads per pass
     static constexpr int kChunks = DP * kBytes / 16;   // 16-byte chunks per row
     static constexpr int kHalf = WP * DP * kBytes;     // bytes of a stage's K (and of its V)
-    static constexpr int kStage = 2 * kHalf;           // = 64 DP: also 16 fp32 rows of DP
-    static constexpr int kQuery = kRows * DP * kBytes;  // bytes of one query buffer
-    static constexpr int kQueries = kHalfType ? ST * kQuery : 2 * kQuery;  // one per stage; fp32: one, as pairs
+    static constexpr int kStage = 2 * kHalf;
     static constexpr int kThreads = NW * 32;
-    static constexpr bool kQueryRegs = kHalfType && MT * DP <= 128;
+    // the query: a ring of buffers that cp.async fills ahead; fp32: one, as (hi, lo) pairs
+    static constexpr int kQuery = kHeads * DP * kBytes;
+    static constexpr int kQueries = kHalfType ? ST * kQuery : 2 * kQuery;
+    static constexpr bool kQueryRegs = NH * DP * kBytes * kBytes <= 1024;  // at most 32 registers
     static constexpr size_t kSmem = (size_t)NW * ST * kStage + kQueries;
-    static_assert(kStage == 16 * DP * 4, "a stage holds one block of fp32 rows");
+    static_assert(kStage >= 16 * DP * 4, "a stage holds 16 fp32 rows (the merge)");
 };
 
 // How far a logit (base 2) may exceed the running maximum before the sums are rescaled.
@@ -254,11 +262,11 @@ __device__ __forceinline__ float finite_or_zero_max(float m) { return m == -INFI
 template <class S>
 __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(const __grid_constant__ AttentionArgs a) {
     using T = typename S::T;
-    constexpr int DP = S::DP, MT = S::MT, NW = S::NW, ST = S::ST, WP = S::WP, TILE = S::TILE;
+    constexpr int DP = S::DP, NH = S::NH, NW = S::NW, ST = S::ST, WP = S::WP, TILE = S::TILE;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int64_t s_scan[NW], s_at[2];
-    __shared__ int s_where[4];
-    __shared__ float2 s_stat[NW][S::kRows];        // maximum and sum of each warp's rows at a merge
+    __shared__ int64_t s_scan[NW];
+    __shared__ int s_where[3];
+    __shared__ float2 s_stat[NW][S::kHeads];       // maximum and sum of each warp's heads at a merge
     __shared__ uint32_t s_held[ST][NW];            // bit r: position r of the warp's stage counts
     __shared__ longlong2 s_row[NW][WP];            // addresses of the K and V rows being copied
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         }
         const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
         if ((int64_t)blockIdx.x >= ctas) {
-            if (tid == 0) workspace_at<S::kRows, DP>(a.partial, gridDim.x).spill[blockIdx.x] = make_int4(0, 0, 0, 0);
+            if (tid == 0) workspace_at<S::kHeads, DP>(a.partial, gridDim.x).spill[blockIdx.x] = make_int4(0, 0, 0, 0);
             return;
         }
         shares = Shares(total, ctas);
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         count = shares.begin((int64_t)blockIdx.x + 1) - begin;
         if (begin >= upto - mine && begin < upto) {
             int64_t rest = begin - (upto - mine);
-            int b = b0, nt = 0;
+            int b = b0, nt = 1;
             for (; b < b1; ++b) {
                 nt = tiles_of(local_length(a.sh, a.seq_lens[b], a.kv.capacity), TILE);
                 if (rest < (int64_t)nt * a.head_blocks) break;
@@ -341,7 +349,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     // One warp-wide copy covers kRowsPerCopy rows (or a 32-chunk part of one).  Chunk c of row r lies
     // at chunk c ^ (r mod 8) of its row in shared memory, so that the 8 rows of an ldmatrix, or
     // of a fragment's float reads, fall into different banks.
-    constexpr int kRowsPerCopy = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;  // rows per warp-wide copy
+    constexpr int kRowsPerCopy = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;
     constexpr int kCopiesPerRow = S::kChunks > 32 ? S::kChunks / 32 : 1;
     const int my_row = S::kChunks > 32 ? 0 : lane / S::kChunks, my_chunk = S::kChunks > 32 ? lane : lane % S::kChunks;
     const uint32_t lane_to = my_row * S::kChunks * 16, lane_sw = (uint32_t)(my_chunk ^ my_row) << 4;
@@ -350,12 +358,12 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     // request or head block) and moves on.
     auto copy_next = [&](bool first) {
         if (S::kHalfType && (first || ld.t == 0)) {
-            const int row0 = ld.rb * S::kRows;
+            const int head0 = ld.rb * S::kHeads;
             const uint32_t dst = queries + ld_query * S::kQuery;
-            const uint32_t *src = a.q + ld.b * a.q_sb_w + (int64_t)(ld.kvh * a.group + row0) * a.q_sh_w;
-            for (int i = tid; i < S::kRows * S::kChunks; i += S::kThreads) {
+            const uint32_t *src = a.q + ld.b * a.q_sb_w + (int64_t)(ld.kvh * a.group + head0) * a.q_sh_w;
+            for (int i = tid; i < S::kHeads * S::kChunks; i += S::kThreads) {
                 const int r = i / S::kChunks, c = i - r * S::kChunks;
-                const bool in = row0 + r < a.group && c * 4 < a.kv.data_w;
+                const bool in = head0 + r < a.group && c * 4 < a.kv.data_w;
                 cp_async_or_zero(dst + (r * S::kChunks + (c ^ (r & 7))) * 16, in ? src + r * a.q_sh_w + c * 4 : a.q, in);
             }
             ld_query = ld_query + 1 == ST ? 0 : ld_query + 1;
@@ -380,7 +388,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
             for (int i = 0; i < WP * S::kChunks / 32; ++i) {
                 const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
                 const longlong2 at = s_row[warp][row0 + my_row];
-                // row0 + my_row mod 8 = (row0 mod 8) ^ my_row: my_row < kRowsPerCopy, which divides row0
+                // (row0 + my_row) mod 8 = (row0 mod 8) ^ my_row: my_row < kRowsPerCopy, which divides row0
                 const uint32_t to = dst + ((lane_sw ^ ((row0 & 7) << 4)) + (row0 * S::kChunks + c0) * 16);
                 const char *k = reinterpret_cast<const char *>(at.x) + (my_chunk + c0) * 16;
                 const char *v = reinterpret_cast<const char *>(at.y) + (my_chunk + c0) * 16;
@@ -404,23 +412,31 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         cp_async_commit();
     }
 
+    // The state of this warp's positions: o[h][j] holds columns 16 j + g (+ 8) of heads 8 h + 2 t4 (+ 1);
+    // m and sum (this lane's part) of those two heads.  A logit x (base 2) enters as
+    // 2^(x + raise), raise = shift - m; with no logit yet raise is +inf, which sends the first tile
+    // through the slow path below.
     const float scale2 = a.scale * kLog2e;
     const int g = lane >> 2, t4 = lane & 3;
-    const bool upper = a.group > 8;  // rows 8..15 of a block hold query heads
-    float o[MT][DP / 8][4], m[MT][2], sum[MT][2];
-    uint32_t qf[S::kQueryRegs ? MT : 1][S::kQueryRegs ? DP / 16 : 1][4];
+    constexpr float kShift = WeightShift<T>::value;
+    float o[NH][DP / 16][4], m[NH][2], raise[NH][2], sum[NH][2];
+    uint32_t qf[S::kQueryRegs ? NH : 1][S::kQueryRegs ? DP * S::kBytes / 32 : 1][S::kHalfType ? 2 : 4];
     int cp_query = 0, cp_stage = 0, first_t = cp.t;
     uint32_t query = queries;
-    // ldmatrix places of this lane: K rows for the first product, V rows (transposed) for the second.
-    // Chunk 2 j + e of row r lies at ((2 j + e) ^ (r mod 8)): 16-byte steps that depend on j mod 4
-    // through these, the rest is a constant 128 (j / 4).
+    // Places of this lane in a stage: ldmatrix rows of K (16-bit) or its floats of K (fp32), and of V.
+    // Chunk c of row r lies at c ^ (r mod 8): of c = 2 j + e the part that depends on j mod 4 is in
+    // these, the rest is a constant 128 (j / 4).
     uint32_t k_at[4], v_at[4];
-    {
-        const int rk = (lane & 7) + ((lane >> 4) << 3), rv = lane & 15;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            k_at[j] = rk * (DP * 2) + (((2 * j + ((lane >> 3) & 1)) ^ (rk & 7)) << 4);
-            v_at[j] = S::kHalf + rv * (DP * 2) + (((2 * j + (lane >> 4)) ^ (rv & 7)) << 4);
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (S::kHalfType) {
+            const int rk = lane & 15, rv = (lane & 7) + ((lane >> 4) << 3);
+            k_at[j] = rk * (DP * 2) + (((2 * j + (lane >> 4)) ^ (rk & 7)) << 4);
+            v_at[j] = S::kHalf + rv * (DP * 2) + (((2 * j + ((lane >> 3) & 1)) ^ (rv & 7)) << 4);
+        } else {
+            k_at[j] = g * (DP * 4) + (((2 * j) ^ g) << 4) + t4 * 4;
+            // position 2 t4 (the next one's chunks differ in bit 0), column 8 j + g
+            v_at[j] = S::kHalf + 2 * t4 * (DP * 4) + (((2 * j + (g >> 2)) ^ (2 * t4)) << 4) + (g & 3) * 4;
         }
     }
 
@@ -436,223 +452,250 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                 cp_query = cp_query + 1 == ST ? 0 : cp_query + 1;
                 if constexpr (S::kQueryRegs) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int h = 0; h < NH; ++h)
 #pragma unroll
-                        for (int ks = 0; ks < DP / 16; ++ks) {
-                            const int r = mt * 16 + (lane & 15), c = 2 * ks + (lane >> 4);
-                            ldmatrix4(qf[mt][ks], query + (r * S::kChunks + (c ^ (r & 7))) * 16);
+                        for (int ks = 0; ks < DP / 16; ks += 2) {
+                            uint32_t q[4];
+                            ldmatrix4(q, query + ((h * 8 + (lane & 7)) * S::kChunks +
+                                                  ((2 * ks + (lane >> 3)) ^ (lane & 7))) * 16);
+                            qf[h][ks][0] = q[0], qf[h][ks][1] = q[1], qf[h][ks + 1][0] = q[2], qf[h][ks + 1][1] = q[3];
                         }
                 }
             } else {
-                // the query as (hi, lo) pairs, split once: row r, element d at r * DP + (d ^ 4 (r mod 8))
-                const int row0 = cp.rb * S::kRows;
-                const uint32_t *src = a.q + cp.b * a.q_sb_w + (int64_t)(cp.kvh * a.group + row0) * a.q_sh_w;
-                for (int x = tid; x < S::kRows * DP; x += S::kThreads) {
-                    const int r = x / DP, d = x - r * DP;
-                    const bool in = row0 + r < a.group && d < a.kv.data_w;
+                // (hi, lo) pairs, split once: head r, element d at r * DP + (d ^ 4 (r mod 8))
+                const int head0 = cp.rb * S::kHeads;
+                const uint32_t *src = a.q + cp.b * a.q_sb_w + (int64_t)(cp.kvh * a.group + head0) * a.q_sh_w;
+                constexpr int kEach = (S::kHeads * DP + S::kThreads - 1) / S::kThreads;
+                float v[kEach];  // all in flight together
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    const int x = tid + e * S::kThreads, r = x / DP, d = x - r * DP;
+                    const bool in = head0 + r < a.group && r < S::kHeads && d < a.kv.data_w;
+                    v[e] = in ? __uint_as_float(__ldg(src + r * a.q_sh_w + d)) : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    const int x = tid + e * S::kThreads, r = x / DP, d = x - r * DP;
                     uint2 pair;
-                    tf32_split(in ? __uint_as_float(src[r * a.q_sh_w + d]) : 0.f, pair.x, pair.y);
-                    query_pairs[r * DP + (d ^ ((r & 7) << 2))] = pair;
+                    tf32_split(v[e], pair.x, pair.y);
+                    if (r < S::kHeads) query_pairs[r * DP + (d ^ ((r & 7) << 2))] = pair;
                 }
                 __syncthreads();
+                if constexpr (S::kQueryRegs) {
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int ks = 0; ks < DP / 8; ++ks) {
+                            const uint2 *q = query_pairs + (h * 8 + g) * DP + t4;
+                            const uint2 q0 = q[((2 * ks) ^ g) * 4], q1 = q[((2 * ks + 1) ^ g) * 4];
+                            qf[h][ks][0] = q0.x, qf[h][ks][1] = q1.x, qf[h][ks][2] = q0.y, qf[h][ks][3] = q1.y;
+                        }
+                }
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                m[mt][0] = m[mt][1] = -INFINITY;
-                sum[mt][0] = sum[mt][1] = 0.f;
+            for (int h = 0; h < NH; ++h) {
 #pragma unroll
-                for (int j = 0; j < DP / 8; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
+                for (int e = 0; e < 2; ++e) {
+                    m[h][e] = -INFINITY;
+                    raise[h][e] = INFINITY;
+                    sum[h][e] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < DP / 16; ++j) o[h][j][0] = o[h][j][1] = o[h][j][2] = o[h][j][3] = 0.f;
             }
         } else {
             __syncwarp();
         }
         const int p0 = cp.t * TILE + warp * WP;
         if (p0 < cp.n) {
-            constexpr int NT = WP / 8;  // 8-position blocks of the product
             const uint32_t stage = stages + cp_stage * S::kStage;
             const uint32_t held = s_held[cp_stage][warp];
-            float x[MT][NT][4];
-            // ---- x = q . k
+            const bool held0 = (held >> g) & 1u, held1 = (held >> (g + 8)) & 1u;
+            // ---- x = K q^T: x[h][0, 1] position g and heads 2 t4, 2 t4 + 1; x[h][2, 3] position g + 8
+            float x[NH][4];
             if constexpr (S::kHalfType) {
+                float x1[NH][4];  // odd steps, to halve the chain of dependent products
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[mt][0][e] = x[mt][NT - 1][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) x[h][e] = x1[h][e] = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks) {
-                    uint32_t kb[4];
-                    ldmatrix4(kb, stage + k_at[ks & 3] + (ks >> 2) * 128);
+                for (int ks = 0; ks < DP / 16; ks += 2) {
+                    uint32_t k0[4], k1[4];
+                    ldmatrix4(k0, stage + k_at[ks & 3] + (ks >> 2) * 128);
+                    ldmatrix4(k1, stage + k_at[(ks + 1) & 3] + (ks >> 2) * 128);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        uint32_t qa[4];
+                    for (int h = 0; h < NH; ++h) {
+                        uint32_t q[4];
                         if constexpr (S::kQueryRegs) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) qa[e] = qf[mt][ks][e];
+                            q[0] = qf[h][ks][0], q[1] = qf[h][ks][1], q[2] = qf[h][ks + 1][0], q[3] = qf[h][ks + 1][1];
                         } else {
-                            const int qr = mt * 16 + (lane & 15), c = 2 * ks + (lane >> 4);
-                            ldmatrix4(qa, query + (qr * S::kChunks + (c ^ (qr & 7))) * 16);
+                            ldmatrix4(q, query + ((h * 8 + (lane & 7)) * S::kChunks +
+                                                  ((2 * ks + (lane >> 3)) ^ (lane & 7))) * 16);
                         }
-                        mma(T{}, x[mt][0], qa, kb[0], kb[1]);
-                        mma(T{}, x[mt][NT - 1], qa, kb[2], kb[3]);
+                        mma(T{}, x[h], k0, q[0], q[1]);
+                        mma(T{}, x1[h], k1, q[2], q[3]);
                     }
                 }
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[h][e] += x1[h][e];
             } else {
                 // three tf32 products: hi hi + hi lo + lo hi (lo lo is below 2^-22 of the product)
-                float x1[4] = {0.f, 0.f, 0.f, 0.f}, x2[4] = {0.f, 0.f, 0.f, 0.f};
+                float x1[NH][4], x2[NH][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[0][0][e] = 0.f;
-                const float *kr = reinterpret_cast<const float *>(smem + (stage - smem_addr(smem))) + g * DP + t4;
-                const uint2 *qr = query_pairs + g * DP + t4;
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[h][e] = x1[h][e] = x2[h][e] = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < DP / 8; ++ks) {
-                    const int c0 = ((2 * ks) ^ g) * 4, c1 = ((2 * ks + 1) ^ g) * 4;
-                    uint32_t kh[2], kl[2];
-                    tf32_split(kr[c0], kh[0], kl[0]);
-                    tf32_split(kr[c1], kh[1], kl[1]);
-                    const uint2 q0 = qr[c0], q1 = upper ? qr[8 * DP + c0] : make_uint2(0u, 0u), q2 = qr[c1],
-                                q3 = upper ? qr[8 * DP + c1] : make_uint2(0u, 0u);
-                    const uint32_t qh[4] = {q0.x, q1.x, q2.x, q3.x}, ql[4] = {q0.y, q1.y, q2.y, q3.y};
-                    mma(T{}, x[0][0], qh, kh[0], kh[1]);
-                    mma(T{}, x1, qh, kl[0], kl[1]);
-                    mma(T{}, x2, ql, kh[0], kh[1]);
+                    const uint32_t at = stage - smem_addr(smem) + k_at[ks & 3] + (ks >> 2) * 128, next = at ^ 16;
+                    uint32_t kh[4], kl[4];
+                    tf32_split(*reinterpret_cast<const float *>(smem + at), kh[0], kl[0]);
+                    tf32_split(*reinterpret_cast<const float *>(smem + at + 8 * DP * 4), kh[1], kl[1]);
+                    tf32_split(*reinterpret_cast<const float *>(smem + next), kh[2], kl[2]);
+                    tf32_split(*reinterpret_cast<const float *>(smem + next + 8 * DP * 4), kh[3], kl[3]);
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        uint32_t q[4];
+                        if constexpr (S::kQueryRegs) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) q[e] = qf[h][ks][e];
+                        } else {
+                            const uint2 *qp = query_pairs + (h * 8 + g) * DP + t4;
+                            const uint2 q0 = qp[((2 * ks) ^ g) * 4], q1 = qp[((2 * ks + 1) ^ g) * 4];
+                            q[0] = q0.x, q[1] = q1.x, q[2] = q0.y, q[3] = q1.y;
+                        }
+                        mma(T{}, x[h], kh, q[0], q[1]);
+                        mma(T{}, x1[h], kh, q[2], q[3]);
+                        mma(T{}, x2[h], kl, q[0], q[1]);
+                    }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[0][0][e] += x1[e] + x2[e];
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[h][e] += x1[h][e] + x2[h][e];
             }
-            // ---- logits
+            // ---- logits: 8 lanes write 8 adjacent positions of a head
             if (a.logits_cap) {
-                const int row0 = cp.rb * S::kRows, end = min(cp.n, a.logits_cap);
+                const int end = min(cp.n, a.logits_cap), p = p0 + g;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int r = row0 + mt * 16 + half * 8 + g;
-                        if (r >= a.group) continue;
-                        float *to = a.logits + cp.b * a.logits_sb + (int64_t)(cp.kvh * a.group + r) * a.logits_sh + p0;
+                    for (int e = 0; e < 2; ++e) {
+                        const int head = cp.rb * S::kHeads + h * 8 + 2 * t4 + e;
+                        if (head >= a.group) continue;
+                        float *to = a.logits + cp.b * a.logits_sb + (int64_t)(cp.kvh * a.group + head) * a.logits_sh + p;
+                        if (p < end) to[0] = held0 ? x[h][e] * a.scale : -INFINITY;
+                        if (p + 8 < end) to[8] = held1 ? x[h][2 + e] * a.scale : -INFINITY;
+                    }
+            }
+            // ---- weights 2^(x scale2 + raise).  The maximum m moves only when a logit exceeds it by more
+            // than kSlack: weights up to 2^kSlack are as exact, and neither the reduction over
+            // the warp nor the rescale is needed in the usual tile.
+            float w[NH][4];
+            bool usual = true;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const int c = nt * 8 + 2 * t4;
-                            const float v0 = (held >> c) & 1u ? x[mt][nt][2 * half] * a.scale : -INFINITY;
-                            const float v1 = (held >> (c + 1)) & 1u ? x[mt][nt][2 * half + 1] * a.scale : -INFINITY;
-                            if (a.logits_pairs && p0 + WP <= end) {
-                                *reinterpret_cast<float2 *>(to + c) = make_float2(v0, v1);
-                            } else {
-                                if (p0 + c < end) to[c] = v0;
-                                if (p0 + c + 1 < end) to[c + 1] = v1;
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[h][e] = fmaf(x[h][e], scale2, raise[h][e & 1]);
+                    if (held != (1u << WP) - 1u && !(e < 2 ? held0 : held1)) w[h][e] = -INFINITY;
+                    usual = usual && w[h][e] <= kSlack + kShift;  // false for NaN
+                }
+            if (!__all_sync(0xffffffffu, usual)) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y0 = held0 ? x[h][e] * scale2 : -INFINITY, y1 = held1 ? x[h][2 + e] * scale2 : -INFINITY;
+                        float top = fmaxf(y0, y1);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        if (top > m[h][e] + kSlack) {
+                            const float keep = exp2_fast(m[h][e] - top);  // 0 when there was no logit
+                            m[h][e] = top;
+                            raise[h][e] = kShift - top;
+                            sum[h][e] *= keep;
+#pragma unroll
+                            for (int j = 0; j < DP / 16; ++j) {
+                                o[h][j][e] *= keep;
+                                o[h][j][2 + e] *= keep;
                             }
                         }
+                        // no finite logit yet: -inf gives 0, NaN gives NaN
+                        const float add = m[h][e] == -INFINITY ? 0.f : raise[h][e];
+                        w[h][e] = y0 + add;
+                        w[h][2 + e] = y1 + add;
                     }
             }
-            // ---- base-2 logits, masked
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int h = 0; h < NH; ++h) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[mt][nt][e] *= scale2;
-            if (held != (1u << WP) - 1u) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!((held >> (nt * 8 + 2 * t4 + (e & 1))) & 1u)) x[mt][nt][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e) w[h][e] = exp2_fast(w[h][e]);
+                sum[h][0] += w[h][0] + w[h][2];
+                sum[h][1] += w[h][1] + w[h][3];
             }
-            // ---- running maximum and weights.  The maximum m moves only when a logit exceeds it by more
-            // than kSlack: weights up to 2^kSlack are as exact, and the rescale is nearly never needed.
-            bool grew = false;
-            float keep[MT][2];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    keep[mt][half] = 1.f;
-                    if (half == 1 && !upper) {  // no query heads there: zero weights
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) x[mt][nt][2] = x[mt][nt][3] = 0.f;
-                        continue;
-                    }
-                    float top = fmaxf(x[mt][0][2 * half], x[mt][0][2 * half + 1]);
-                    if (NT == 2) top = fmaxf(top, fmaxf(x[mt][NT - 1][2 * half], x[mt][NT - 1][2 * half + 1]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float old = m[mt][half];
-                    if (top > old + kSlack) {
-                        grew = true;
-                        m[mt][half] = top;
-                        keep[mt][half] = exp2_fast(old - top);
-                    }
-                    const float base = finite_or_zero_max(m[mt][half]) - WeightShift<T>::value;
-                    float add = 0.f;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float &v = x[mt][nt][2 * half + e];
-                            v = exp2_fast(v - base);
-                            add += v;
-                        }
-                    sum[mt][half] = fmaf(sum[mt][half], keep[mt][half], add);
-                }
-            if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int j = 0; j < DP / 8; ++j) {
-                        o[mt][j][0] *= keep[mt][0];
-                        o[mt][j][1] *= keep[mt][0];
-                        o[mt][j][2] *= keep[mt][1];
-                        o[mt][j][3] *= keep[mt][1];
-                    }
-            }
-            // ---- o += weights . v, each weight as two parts of the element type
+            // ---- o^T += V^T w^T, each weight as two parts of the element type
             if constexpr (S::kHalfType) {
-                uint32_t hi[MT][4], lo[MT][4];
+                uint32_t hi[NH][2], lo[NH][2];  // positions 2 t4, 2 t4 + 1 (+ 8) of head g
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int h = 0; h < NH; ++h)
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const float *w = &x[mt][f >> 1][2 * (f & 1)];
+                    for (int f = 0; f < 2; ++f) {
                         float back[2], rest[2];
-                        hi[mt][f] = T::encode(w);
-                        T::decode(hi[mt][f], back);
-                        rest[0] = w[0] - back[0];
-                        rest[1] = w[1] - back[1];
-                        lo[mt][f] = T::encode(rest);
+                        const uint32_t top = T::encode(&w[h][2 * f]);
+                        T::decode(top, back);
+                        rest[0] = w[h][2 * f] - back[0];
+                        rest[1] = w[h][2 * f + 1] - back[1];
+                        hi[h][f] = transpose8x8(top);
+                        lo[h][f] = transpose8x8(T::encode(rest));
                     }
 #pragma unroll
                 for (int j = 0; j < DP / 16; ++j) {
-                    uint32_t vb[4];
-                    ldmatrix4_trans(vb, stage + v_at[j & 3] + (j >> 2) * 128);
+                    uint32_t v[4];
+                    ldmatrix4_trans(v, stage + v_at[j & 3] + (j >> 2) * 128);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma(T{}, o[mt][2 * j], hi[mt], vb[0], vb[1]);
-                        mma(T{}, o[mt][2 * j + 1], hi[mt], vb[2], vb[3]);
-                        mma(T{}, o[mt][2 * j], lo[mt], vb[0], vb[1]);
-                        mma(T{}, o[mt][2 * j + 1], lo[mt], vb[2], vb[3]);
-                    }
+                    for (int h = 0; h < NH; ++h) mma(T{}, o[h][j], v, hi[h][0], hi[h][1]);
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) mma(T{}, o[h][j], v, lo[h][0], lo[h][1]);
                 }
             } else {
-                // the k index of the product runs over positions in the order 0 2 4 6 1 3 5 7, which
-                // is how the weights lie in the registers of the first product
-                uint32_t wh[4], wl[4];
-                tf32_split(x[0][0][0], wh[0], wl[0]);
-                tf32_split(x[0][0][2], wh[1], wl[1]);
-                tf32_split(x[0][0][1], wh[2], wl[2]);
-                tf32_split(x[0][0][3], wh[3], wl[3]);
-                const float *v0 = reinterpret_cast<const float *>(smem + (stage + S::kHalf - smem_addr(smem))) +
-                                  (2 * t4) * DP + (g & 3);
+                // two steps of 8 positions, in the order 0 2 4 6 1 3 5 7; the weights of position 2 t4 (+ 1)
+                // and head g come from the lane that holds them
+                uint32_t wh[NH][2][2], wl[NH][2][2];
 #pragma unroll
-                for (int j = 0; j < DP / 8; ++j) {
-                    const int c = 2 * j + (g >> 2);
-                    uint32_t vh[2], vl[2];
-                    tf32_split(v0[(c ^ (2 * t4)) * 4], vh[0], vl[0]);
-                    tf32_split(v0[DP + (c ^ (2 * t4 + 1)) * 4], vh[1], vl[1]);
-                    mma(T{}, o[0][j], wh, vh[0], vh[1]);
-                    mma(T{}, o[0][j], wh, vl[0], vl[1]);
-                    mma(T{}, o[0][j], wl, vh[0], vh[1]);
-                }
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int from = 8 * t4 + 4 * e + (g >> 1);
+                            const float even = __shfl_sync(0xffffffffu, w[h][2 * f], from);
+                            const float odd = __shfl_sync(0xffffffffu, w[h][2 * f + 1], from);
+                            tf32_split(g & 1 ? odd : even, wh[h][f][e], wl[h][f][e]);
+                        }
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int j = 0; j < DP / 16; ++j) {
+                        // columns 16 j + g and, 2 chunks on, 16 j + 8 + g; position 2 t4 + 1 is a row on, its chunks
+                        // differ in bit 0
+                        const uint32_t base = stage - smem_addr(smem) + f * (8 * DP * 4) + (j >> 1) * 128;
+                        const uint32_t c0 = base + v_at[(2 * j) & 3], c1 = base + v_at[(2 * j + 1) & 3];
+                        uint32_t vh[4], vl[4];
+                        tf32_split(*reinterpret_cast<const float *>(smem + c0), vh[0], vl[0]);
+                        tf32_split(*reinterpret_cast<const float *>(smem + c1), vh[1], vl[1]);
+                        tf32_split(*reinterpret_cast<const float *>(smem + (c0 ^ 16) + DP * 4), vh[2], vl[2]);
+                        tf32_split(*reinterpret_cast<const float *>(smem + (c1 ^ 16) + DP * 4), vh[3], vl[3]);
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            mma(T{}, o[h][j], vh, wh[h][f][0], wh[h][f][1]);
+                            mma(T{}, o[h][j], vh, wl[h][f][0], wl[h][f][1]);
+                            mma(T{}, o[h][j], vl, wh[h][f][0], wh[h][f][1]);
+                        }
+                    }
             }
         }
         __syncwarp();
@@ -660,58 +703,59 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         // ---- the end of a request, or of the share: merge the warps
         const bool last = cp.t + 1 == cp.nt;
         if (last || i + 1 == count) {
-            const int kvh = cp.kvh, row0 = cp.rb * S::kRows;
+            const int head0 = cp.rb * S::kHeads;
             const bool whole = last && first_t == 0;
-            const Workspace ws = workspace_at<S::kRows, DP>(a.partial, gridDim.x);
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (first_t == 0 ? 1 : 0);
+            const Workspace ws = workspace_at<S::kHeads, DP>(a.partial, gridDim.x);
+            const int64_t part = 2 * (int64_t)blockIdx.x + (first_t == 0 ? 1 : 0);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float s = sum[mt][half];
-                    s += __shfl_xor_sync(0xffffffffu, s, 1);
-                    s += __shfl_xor_sync(0xffffffffu, s, 2);
-                    if (t4 == 0) s_stat[warp][mt * 16 + half * 8 + g] = make_float2(m[mt][half], s);
+                for (int e = 0; e < 2; ++e) {
+                    float s = sum[h][e];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                    if (g == 0) s_stat[warp][h * 8 + 2 * t4 + e] = make_float2(m[h][e], s);
                 }
-                // this tile's stage is free until the next copy_next: 16 fp32 rows
-                uint8_t *mine = smem + (size_t)(warp * ST + cp_stage) * S::kStage;
 #pragma unroll
-                for (int j = 0; j < DP / 8; ++j)
+            for (int h0 = 0; h0 < NH; h0 += 2) {  // 16 fp32 rows fit this tile's stage, free until the next copy_next
+                float *mine = reinterpret_cast<float *>(smem + (size_t)(warp * ST + cp_stage) * S::kStage);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int r = half * 8 + g, c = 2 * j + (t4 >> 1);
-                        *reinterpret_cast<float2 *>(mine + r * (DP * 4) + ((c ^ (r & 7)) << 4) + (t4 & 1) * 8) =
-                            make_float2(o[mt][j][2 * half], o[mt][j][2 * half + 1]);
-                    }
+                for (int h = h0; h < h0 + 2 && h < NH; ++h)
+#pragma unroll
+                    for (int j = 0; j < DP / 16; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // row r, column d at d ^ 8 (r / 2 mod 4): the lanes' rows fall into different banks
+                            const int r = (h - h0) * 8 + 2 * t4 + (e & 1), d = 16 * j + 8 * (e >> 1) + g;
+                            mine[r * DP + (d ^ (t4 << 3))] = o[h][j][e];
+                        }
                 __syncthreads();
-                const int rows = min(16, a.group - row0 - mt * 16);
+                const int rows = min(16, min(S::kHeads, a.group - head0) - h0 * 8);
                 for (int x = tid; x < rows * (DP / 4); x += S::kThreads) {
                     const int r = x / (DP / 4), c = x - r * (DP / 4);
-                    float2 st[NW];
                     float top = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) {
-                        st[w] = s_stat[w][mt * 16 + r];
-                        top = fmaxf(top, st[w].x);
-                    }
+                    for (int w = 0; w < NW; ++w) top = fmaxf(top, s_stat[w][h0 * 8 + r].x);
                     const float base = finite_or_zero_max(top);
                     float total = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
-                        const float f = exp2_fast(st[w].x - base);
+                        const float2 st = s_stat[w][h0 * 8 + r];
+                        const float f = exp2_fast(st.x - base);
                         const float4 v = *reinterpret_cast<const float4 *>(
-                            smem + (size_t)(w * ST + cp_stage) * S::kStage + r * (DP * 4) + ((c ^ (r & 7)) << 4));
-                        total = fmaf(st[w].y, f, total);
+                            reinterpret_cast<const float *>(smem + (size_t)(w * ST + cp_stage) * S::kStage) + r * DP +
+                            ((c * 4) ^ (((r >> 1) & 3) << 3)));
+                        total = fmaf(st.y, f, total);
                         acc.x = fmaf(v.x, f, acc.x);
                         acc.y = fmaf(v.y, f, acc.y);
                         acc.z = fmaf(v.z, f, acc.z);
                         acc.w = fmaf(v.w, f, acc.w);
                     }
                     if (whole) {
-                        write_result<T>(a, cp.b, kvh * a.group + row0 + mt * 16 + r, c * 4, acc, top, total);
+                        write_result<T>(a, cp.b, cp.kvh * a.group + head0 + h0 * 8 + r, c * 4, acc, top, total);
                     } else {
-                        const int64_t at = slot * S::kRows + mt * 16 + r;
+                        const int64_t at = part * S::kHeads + h0 * 8 + r;
                         *reinterpret_cast<float4 *>(ws.rows + at * DP + c * 4) = acc;
                         if (c == 0) ws.stats[at] = make_float2(top, total);
                     }
@@ -719,7 +763,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                 __syncthreads();
             }
             if (i + 1 == count && tid == 0) {
-                int4 spill = make_int4(0, cp.b, kvh, cp.rb);
+                int4 spill = make_int4(0, cp.b, cp.kvh, cp.rb);
                 // parts: this share and those up to the one with the request's last tile
                 if (first_t == 0 && !last)
                     spill.x = (int)(shares.of(begin + i + (cp.nt - 1 - cp.t)) - blockIdx.x) + 1;
@@ -794,7 +838,7 @@ int32_t launch_attention(dcp::AttentionArgs a, cudaStream_t stream) {
     const char *fn = "dcp_paged_attention";
     if (!reserve_smem(dcp::attention_stream_kernel<S>, cache, S::kSmem))
         return fail(DCP_ERR_CUDA, "%s: cannot reserve shared memory", fn);
-    a.row_blocks = (a.group + S::kRows - 1) / S::kRows;
+    a.row_blocks = (a.group + S::kHeads - 1) / S::kHeads;
     a.head_blocks = a.kv.heads * a.row_blocks;
     const int64_t most = (int64_t)sm_count() * S::CTAS;
     const int64_t tiles = (int64_t)a.B * a.head_blocks * (a.kv.capacity / S::TILE + 1);
@@ -804,7 +848,7 @@ int32_t launch_attention(dcp::AttentionArgs a, cudaStream_t stream) {
     if (st != DCP_OK) return st;
     // the join's launch overlaps the stream's end; its blocks wait for it before they read
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, a.group < S::kRows ? a.group : S::kRows);
+    cfg.gridDim = dim3(grid, a.group < S::kHeads ? a.group : S::kHeads);
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
@@ -812,27 +856,31 @@ int32_t launch_attention(dcp::AttentionArgs a, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, dcp::attention_join_kernel<T, S::kRows, S::DP>, a) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, dcp::attention_join_kernel<T, S::kHeads, S::DP>, a) != cudaSuccess)
         return launch_status(fn);
     return launch_status(fn);
 }
 
-// The shape for a group of G query heads per key head and D elements: 64 DP bytes per warp and
-// stage, stages to keep 90 to 200 KB of an SM's shared memory in flight.  Groups over 16 heads take
-// two row blocks per pass where the registers hold them (the cache is then read half as often).
+// The shape for a group of G query heads per key head and D elements.
 template <class T, class F>
 auto with_shape(int32_t group, int32_t head_dim, F &&f) {
+    using dcp::AttentionShape;
     if constexpr (T::kPerWord == 2) {
         if (head_dim <= 64)
-            return group <= 16 ? f(dcp::AttentionShape<T, 64, 1, 4, 5, 2>{}) : f(dcp::AttentionShape<T, 64, 2, 4, 5, 2>{});
+            return group <= 8    ? f(AttentionShape<T, 64, 1, 4, 3, 4>{})
+                   : group <= 16 ? f(AttentionShape<T, 64, 2, 4, 3, 4>{})
+                                 : f(AttentionShape<T, 64, 4, 4, 3, 3>{});
         if (head_dim <= 128)
-            return group <= 16 ? f(dcp::AttentionShape<T, 128, 1, 4, 3, 2>{})
-                               : f(dcp::AttentionShape<T, 128, 2, 8, 3, 1>{});
-        return f(dcp::AttentionShape<T, 256, 1, 4, 3, 1>{});
+            return group <= 8    ? f(AttentionShape<T, 128, 1, 4, 2, 3>{})
+                   : group <= 16 ? f(AttentionShape<T, 128, 2, 4, 2, 3>{})
+                                 : f(AttentionShape<T, 128, 4, 4, 2, 2>{});
+        return group <= 8 ? f(AttentionShape<T, 256, 1, 6, 2, 1>{}) : f(AttentionShape<T, 256, 2, 6, 2, 1>{});
     } else {
-        if (head_dim <= 64) return f(dcp::AttentionShape<T, 64, 1, 4, 5, 2>{});
-        if (head_dim <= 128) return f(dcp::AttentionShape<T, 128, 1, 8, 3, 1>{});
-        return f(dcp::AttentionShape<T, 256, 1, 4, 2, 1>{});
+        if (head_dim <= 64)
+            return group <= 8 ? f(AttentionShape<T, 64, 1, 4, 2, 3>{}) : f(AttentionShape<T, 64, 2, 4, 2, 3>{});
+        if (head_dim <= 128)
+            return group <= 8 ? f(AttentionShape<T, 128, 1, 6, 2, 1>{}) : f(AttentionShape<T, 128, 2, 6, 2, 1>{});
+        return f(AttentionShape<T, 256, 1, 3, 2, 1>{});
     }
 }
 
@@ -847,7 +895,7 @@ template <class T>
 int64_t attention_workspace(int32_t group, int32_t head_dim) {
     return with_shape<T>(group, head_dim, [&](auto shape) {
         using S = decltype(shape);
-        return dcp::workspace_bytes<S::kRows, S::DP>((int64_t)sm_count() * S::CTAS);
+        return dcp::workspace_bytes<S::kHeads, S::DP>((int64_t)sm_count() * S::CTAS);
     });
 }
 
