@@ -775,55 +775,142 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     }
 }
 
-// Merges the parts of a request that several shares hold: block (c, r) row r of the request that
-// starts in share c.  Its 128 threads cover DP / 4 column groups times 512 / DP parts at a time.
-template <class T, int ROWS, int DP>
+// Loads that stay where they are written, so that all of a round's are in flight together.
+__device__ __forceinline__ float4 load_float4(const float *p) {
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float2 load_float2(const float2 *p) {
+    float2 v;
+    asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+
+// Merges the parts of a request that several shares hold: block (c, y) heads 4 y .. 4 y + 3 of the
+// request that starts in share c.  Warp w takes parts w, w + 4, ..., U of them in flight for all four
+// heads at once, with a running maximum; the warps meet in shared memory.
+constexpr int kJoinHeads = 4;
+
+template <class T, int HEADS, int DP>
 __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_constant__ AttentionArgs a) {
-    constexpr int CG = DP / 4, PG = 128 / CG;
-    __shared__ float4 s_acc[PG][CG];
+    constexpr int R = kJoinHeads, LANES = DP / 4 < 32 ? DP / 4 : 32, CV = DP / 4 / LANES;  // CV float4 per lane
+    constexpr int SUB = 32 / LANES;                    // parts side by side in a warp
+    constexpr int U = 8 / CV / SUB > 4 ? 4 : 8 / CV / SUB;
+    __shared__ float4 s_acc[4][R][DP / 4];
+    __shared__ float2 s_st[4][R];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Workspace ws = workspace_at<ROWS, DP>(a.partial, gridDim.x);
+    const Workspace ws = workspace_at<HEADS, DP>(a.partial, gridDim.x);
     const int4 spill = ws.spill[blockIdx.x];
-    const int parts = spill.x, r = blockIdx.y, lane = threadIdx.x & 31;
-    if (parts == 0) return;
-    const int kvh = spill.z, row = spill.w * ROWS + r;
-    if (row >= a.group) return;
-    // part 0 is the share's unfinished request, the others the requests entered in the middle
-    auto slot = [&](int p) { return (int64_t)(2 * ((int64_t)blockIdx.x + p) + (p == 0 ? 1 : 0)) * ROWS + r; };
-    float top = -INFINITY;
-    for (int p = lane; p < parts; p += 32) top = fmaxf(top, ws.stats[slot(p)].x);
-    top = group_max<32>(top);
-    const float base = finite_or_zero_max(top);
-    float total = 0.f;
-    for (int p = lane; p < parts; p += 32) {
-        const float2 st = ws.stats[slot(p)];
-        total = fmaf(st.y, exp2_fast(st.x - base), total);
-    }
-    total = group_sum<32>(total);
-    const int c = threadIdx.x % CG, pg = threadIdx.x / CG;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = pg; p < parts; p += PG) {
-        const int64_t at = slot(p);
-        const float f = exp2_fast(ws.stats[at].x - base);
-        const float4 v = *reinterpret_cast<const float4 *>(ws.rows + at * DP + c * 4);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
-    }
-    s_acc[pg][c] = acc;
-    __syncthreads();
-    if (pg == 0) {
+    const int parts = spill.x, r0 = blockIdx.y * R, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = lane / LANES, c = lane % LANES;
+    const int rows = min(R, min(HEADS, a.group - spill.w * HEADS) - r0);
+    if (parts == 0 || rows <= 0) return;
+    float m[R], sum[R];
+    float4 acc[R][CV];
 #pragma unroll
-        for (int i = 1; i < PG; ++i) {
-            const float4 v = s_acc[i][c];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        sum[r] = 0.f;
+#pragma unroll
+        for (int v = 0; v < CV; ++v) acc[r][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // all lanes of the warp make the same rounds
+    for (int p0 = warp * SUB; p0 < parts; p0 += 4 * SUB * U) {
+        float2 st[U][R];
+        float4 o[U][R][CV];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            // part 0 is the share's unfinished request, the others the requests entered in the middle; a part or
+            // head too many reads the last one and counts nothing
+            const int p = p0 + sub + u * 4 * SUB, pc = min(p, parts - 1);
+            const int64_t at = (int64_t)(2 * ((int64_t)blockIdx.x + pc) + (pc == 0 ? 1 : 0)) * HEADS + r0;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t row = at + min(r, rows - 1);
+                st[u][r] = load_float2(ws.stats + row);
+#pragma unroll
+                for (int v = 0; v < CV; ++v) o[u][r][v] = load_float4(ws.rows + row * DP + (c + v * LANES) * 4);
+            }
         }
-        write_result<T>(a, spill.y, kvh * a.group + row, c * 4, acc, top, total);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float top = m[r];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (p0 + sub + u * 4 * SUB >= parts) st[u][r] = make_float2(-INFINITY, 0.f);
+                top = fmaxf(top, st[u][r].x);
+            }
+            const float base = finite_or_zero_max(top), f0 = exp2_fast(m[r] - base);
+            m[r] = top;
+            sum[r] *= f0;
+#pragma unroll
+            for (int v = 0; v < CV; ++v) {
+                acc[r][v].x *= f0;
+                acc[r][v].y *= f0;
+                acc[r][v].z *= f0;
+                acc[r][v].w *= f0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (p0 + sub + u * 4 * SUB >= parts) continue;  // what was read there may be anything
+                const float f = exp2_fast(st[u][r].x - base);
+                sum[r] = fmaf(st[u][r].y, f, sum[r]);
+#pragma unroll
+                for (int v = 0; v < CV; ++v) {
+                    acc[r][v].x = fmaf(o[u][r][v].x, f, acc[r][v].x);
+                    acc[r][v].y = fmaf(o[u][r][v].y, f, acc[r][v].y);
+                    acc[r][v].z = fmaf(o[u][r][v].z, f, acc[r][v].z);
+                    acc[r][v].w = fmaf(o[u][r][v].w, f, acc[r][v].w);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int d = LANES; d < 32; d <<= 1)  // the warp's halves
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float om = __shfl_xor_sync(0xffffffffu, m[r], d), top = fmaxf(m[r], om);
+            const float base = finite_or_zero_max(top), f0 = exp2_fast(m[r] - base), f1 = exp2_fast(om - base);
+            m[r] = top;
+            sum[r] = fmaf(__shfl_xor_sync(0xffffffffu, sum[r], d), f1, sum[r] * f0);
+#pragma unroll
+            for (int v = 0; v < CV; ++v) {
+                acc[r][v].x = fmaf(__shfl_xor_sync(0xffffffffu, acc[r][v].x, d), f1, acc[r][v].x * f0);
+                acc[r][v].y = fmaf(__shfl_xor_sync(0xffffffffu, acc[r][v].y, d), f1, acc[r][v].y * f0);
+                acc[r][v].z = fmaf(__shfl_xor_sync(0xffffffffu, acc[r][v].z, d), f1, acc[r][v].z * f0);
+                acc[r][v].w = fmaf(__shfl_xor_sync(0xffffffffu, acc[r][v].w, d), f1, acc[r][v].w * f0);
+            }
+        }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (lane == 0) s_st[warp][r] = make_float2(m[r], sum[r]);
+        if (sub == 0)
+#pragma unroll
+            for (int v = 0; v < CV; ++v) s_acc[warp][r][c + v * LANES] = acc[r][v];
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < rows * (DP / 4); x += 128) {
+        const int r = x / (DP / 4), col = x - r * (DP / 4);
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, s_st[w][r].x);
+        const float base = finite_or_zero_max(top);
+        float total = 0.f;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float2 st = s_st[w][r];
+            const float4 v = s_acc[w][r][col];
+            const float f = exp2_fast(st.x - base);
+            total = fmaf(st.y, f, total);
+            t.x = fmaf(v.x, f, t.x);
+            t.y = fmaf(v.y, f, t.y);
+            t.z = fmaf(v.z, f, t.z);
+            t.w = fmaf(v.w, f, t.w);
+        }
+        write_result<T>(a, spill.y, spill.z * a.group + spill.w * HEADS + r0 + r, col * 4, t, top, total);
     }
 }
 
@@ -848,7 +935,8 @@ int32_t launch_attention(dcp::AttentionArgs a, cudaStream_t stream) {
     if (st != DCP_OK) return st;
     // the join's launch overlaps the stream's end; its blocks wait for it before they read
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, a.group < S::kHeads ? a.group : S::kHeads);
+    const int heads = a.group < S::kHeads ? a.group : S::kHeads;
+    cfg.gridDim = dim3(grid, (heads - 1) / dcp::kJoinHeads + 1);
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
