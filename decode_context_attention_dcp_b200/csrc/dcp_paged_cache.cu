@@ -28,27 +28,28 @@ __device__ __forceinline__ void copy_rows(const RowMove *moves, int rows, FastDi
     const int items = rows * (int)chunks.d;
     for (int i0 = threadIdx.x; i0 < items; i0 += U * kCopyThreads) {
         uint4 k[U], v[U];
-        int64_t k_to[U], v_to[U];
+        int at[U];  // row and word; -1: nothing
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u * kCopyThreads;
-            k_to[u] = -1;
+            at[u] = -1;
             if (i < items) {
                 const int r = (int)chunks.div((uint32_t)i), w = (i - r * (int)chunks.d) * 4;
-                const RowMove mv = moves[r];
-                if (mv.k_from >= 0) {
-                    k[u] = *reinterpret_cast<const uint4 *>(k_src + mv.k_from + w);
-                    v[u] = *reinterpret_cast<const uint4 *>(v_src + mv.v_from + w);
-                    k_to[u] = mv.k_to + w;
-                    v_to[u] = mv.v_to + w;
+                const int64_t k_from = moves[r].k_from, v_from = moves[r].v_from;
+                if (k_from >= 0) {
+                    k[u] = *reinterpret_cast<const uint4 *>(k_src + k_from + w);
+                    v[u] = *reinterpret_cast<const uint4 *>(v_src + v_from + w);
+                    at[u] = r << 16 | w;  // w < 256
                 }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (k_to[u] >= 0) {
-                *reinterpret_cast<uint4 *>(k_dst + k_to[u]) = k[u];
-                *reinterpret_cast<uint4 *>(v_dst + v_to[u]) = v[u];
+            if (at[u] >= 0) {
+                const RowMove &mv = moves[at[u] >> 16];
+                const int w = at[u] & 0xffff;
+                *reinterpret_cast<uint4 *>(k_dst + mv.k_to + w) = k[u];
+                *reinterpret_cast<uint4 *>(v_dst + mv.v_to + w) = v[u];
             }
     }
 }
@@ -203,45 +204,67 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelectThreads = 1024;
-constexpr int kBins = 2048;
-
-// Exclusive prefix and total of one value per thread over the block; `sums` is shared scratch.
-__device__ __forceinline__ uint64_t block_prefix(uint64_t mine, uint64_t *sums, uint64_t &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-    }
-    __syncthreads();  // the scratch may still be read from the last call
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    uint64_t s = sums[lane];
-    uint64_t all = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(0xffffffffu, all, o);
-        if (lane >= o) all += x;
-    }
-    total = __shfl_sync(0xffffffffu, all, 31);
-    return upto - mine + __shfl_sync(0xffffffffu, all - s, warp);
+// The weight of a key; zeros and NaN, whose keys have several weights, are read again.
+__device__ __forceinline__ float key_weight(uint32_t key, const float *w) {
+    if (key == 0u || key == 0x80000000u) return __ldg(w);
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// One cluster per (request, key head).  A thread holds KPT adjacent weights; positions past the
-// cluster's CTAs * 1024 * KPT are handled in further rounds that read them again.
-//   threshold: the key of the last kept position, 11 + 11 + 10 bits, one shared-memory histogram
-//   per pass (summed over the cluster through distributed shared memory) and a suffix scan;
+constexpr int kBins = 2048;
+constexpr int kKeys = 16;  // weights per thread
+
+// Exclusive prefix and total of one value per thread over a block of W warps; `sums` is shared scratch.
+template <int W>
+__device__ __forceinline__ uint32_t block_prefix(uint32_t mine, uint32_t *sums, uint32_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    // every warp adds up the W sums
+    const uint32_t own = lane < W ? sums[lane] : 0;
+    uint32_t all = own;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += x;
+    }
+    total = __shfl_sync(0xffffffffu, all, W - 1);
+    return __shfl_sync(0xffffffffu, all - own, warp) + upto - mine;
+}
+
+// How a selection kernel holds a row's weights (as keys):
+//   kRegisters  one CTA, kKeys adjacent weights per thread in registers;
+//   kShared     one CTA, in shared memory: longer rows without a second reading;
+//   kCluster    a cluster of CTAs, in registers; what they cannot hold is read again per pass.
+// Measured at 256 rows of 20000 to 32768 weights: kShared 20 us, kCluster (4 CTAs, a barrier and
+// remote histograms per pass) 72 us; kRegisters and kShared at 24 rows of up to 2000: 7 and 9 us.
+enum KeyStore { kRegisters, kShared, kCluster };
+
+// The kept positions of one (request, key head) row.
+//   threshold: the key of the last kept position, by its 11, 11 and 10 highest bits in turn: a
+//   shared-memory histogram per pass (summed over the cluster through distributed shared memory)
+//   and a prefix sum from the highest bin down;
 //   output: keys above it and the first ties are placed by a prefix sum in position order.
-template <int KPT>
-__global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_constant__ EvictArgs a) {
-    __shared__ uint32_t hist[3][kBins];
-    __shared__ uint64_t sums[32];
-    __shared__ uint64_t s_total[2];
+// Positions past the end enter as key 0: below or equal to every weight and after it, they are
+// never among the kept.
+template <int THREADS, int STORE>
+__global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constant__ EvictArgs a) {
+    constexpr bool CLUSTER = STORE == kCluster, SHARED = STORE == kShared;
+    constexpr int W = THREADS / 32, BPT = kBins / THREADS;  // bins per thread
+    static_assert(BPT % 2 == 0 && (SHARED || THREADS * kKeys < 65536), "pairs of bins; 16-bit counts");
+    extern __shared__ uint4 s_keys[];  // kShared: the row's keys, four to a chunk
+    __shared__ __align__(16) uint32_t hist[3][kBins];
+    __shared__ uint32_t sums[4][W];  // one per prefix sum in turn
+    __shared__ uint32_t s_total[1];
     __shared__ uint32_t s_digit, s_need;
     cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), tid = threadIdx.x;
+    const int ctas = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
+    const int tid = threadIdx.x;
     const int row = blockIdx.x / ctas, b = row / a.src.heads, j = row - b * a.src.heads;
     const float *w = a.weights + b * a.w_sb + j * a.w_sh;
     float *nw = a.new_weights + b * a.nw_sb + j * a.nw_sh;
@@ -251,123 +274,232 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const __grid_
     const int m = n < a.keep ? n : a.keep;
     if (j == 0 && rank == 0 && tid == 0) a.new_lens[b] = m;
     const bool full = n <= a.keep;
-    const int body = full ? 0 : n - a.recent;            // positions that compete
+    const uint32_t body = full ? 0 : (uint32_t)(n - a.recent);  // positions that compete
     const uint32_t want = full ? 0 : (uint32_t)(a.keep - a.recent);
-    const int64_t round = (int64_t)ctas * kSelectThreads * KPT;
-    const int64_t mine = ((int64_t)rank * kSelectThreads + tid) * KPT;
+    // registers: this thread's keys start at `mine`, and every `round` after it
+    const uint32_t round = (uint32_t)ctas * THREADS * kKeys;  // below 2^17
+    const uint32_t mine = ((uint32_t)rank * THREADS + tid) * kKeys;
+    const uint32_t chunks = (body + 31) / 32 * 8;  // shared memory: whole warps of keys
 
-    auto load = [&](int64_t p, uint32_t *key) {
-        if (p + KPT <= body && ((reinterpret_cast<uintptr_t>(w + p)) & 15) == 0) {
+    auto load = [&](uint32_t p, uint32_t *key) {
+        if (p + kKeys <= body && (reinterpret_cast<uintptr_t>(w + p) & 15) == 0) {
+            float4 v[kKeys / 4];
 #pragma unroll
-            for (int i = 0; i < KPT; i += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(w + p + i);
-                key[i] = weight_key(v.x), key[i + 1] = weight_key(v.y);
-                key[i + 2] = weight_key(v.z), key[i + 3] = weight_key(v.w);
+            for (int i = 0; i < kKeys / 4; ++i) v[i] = __ldg(reinterpret_cast<const float4 *>(w + p) + i);
+#pragma unroll
+            for (int i = 0; i < kKeys / 4; ++i) {
+                key[4 * i] = weight_key(v[i].x), key[4 * i + 1] = weight_key(v[i].y);
+                key[4 * i + 2] = weight_key(v[i].z), key[4 * i + 3] = weight_key(v[i].w);
             }
         } else {
+            float v[kKeys];
 #pragma unroll
-            for (int i = 0; i < KPT; ++i) key[i] = p + i < body ? weight_key(w[p + i]) : 0u;
+            for (int i = 0; i < kKeys; ++i) v[i] = p + i < body ? __ldg(w + p + i) : 0.f;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) key[i] = p + i < body ? weight_key(v[i]) : 0u;
         }
     };
-    uint32_t first[KPT];
-    uint32_t prefix = 0, need = want;
+    uint32_t first[SHARED ? 1 : kKeys];
     if (want) {
-        load(mine, first);
-        for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
-        __syncthreads();
+        for (int i = tid; i < 3 * kBins / 4; i += THREADS) reinterpret_cast<uint4 *>(&hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+        if constexpr (SHARED) {
+            const bool vec = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+            constexpr int U = 8;
+            for (uint32_t c0 = tid; c0 < chunks; c0 += U * THREADS) {
+                float v[U][4];
 #pragma unroll
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            for (int64_t p0 = mine; p0 < body; p0 += round) {
-                uint32_t again[KPT];
-                if (p0 != mine) load(p0, again);
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t p = 4 * (c0 + u * THREADS);
+                    if (vec && p + 4 <= body) {
+                        const float4 f = __ldg(reinterpret_cast<const float4 *>(w + p));
+                        v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
+                    } else {
 #pragma unroll
-                for (int i = 0; i < KPT; ++i) {
-                    const uint32_t key = p0 == mine ? first[i] : again[i];
-                    const bool in = p0 + i < body && (pass == 0 || (key >> (shift + bits)) == (prefix >> (shift + bits)));
-                    if (in) atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1u)], 1u);
+                        for (int e = 0; e < 4; ++e) v[u][e] = p + e < body ? __ldg(w + p + e) : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t c = c0 + u * THREADS;
+                    uint32_t k[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) k[e] = 4 * c + e < body ? weight_key(v[u][e]) : 0u;
+                    if (c < chunks) s_keys[c] = make_uint4(k[0], k[1], k[2], k[3]);
                 }
             }
-            cluster.sync();
-            // bins in descending order: thread t holds bins kBins - 1 - 2t and the one below
-            uint32_t c[2] = {0, 0};
-            const int top = kBins - 1 - 2 * tid;
-            for (int r = 0; r < ctas; ++r) {
-                const uint32_t *other = ctas == 1 ? &hist[pass][0] : cluster.map_shared_rank(&hist[pass][0], r);
-                c[0] += other[top];
-                c[1] += other[top - 1];
-            }
-            uint64_t total;
-            const uint32_t above = (uint32_t)block_prefix(c[0] + c[1], sums, total);
-            if (above < need && need <= above + c[0] + c[1]) {
-                const bool low = need > above + c[0];
-                s_digit = (uint32_t)(low ? top - 1 : top);
-                s_need = need - above - (low ? c[0] : 0);
-            }
-            __syncthreads();
-            prefix |= s_digit << shift;
-            need = s_need;
-        }
-    }
-    // keys above `prefix` are kept, and the first `need` that equal it
-    uint64_t before = 0;  // (ties << 32 | above) in earlier rounds
-    if (want)
-    for (int64_t q = 0; q < body; q += round) {
-        const int64_t p = q + mine;
-        uint32_t key[KPT];
-        uint64_t count = 0;
-        if (q == 0) {
-#pragma unroll
-            for (int i = 0; i < KPT; ++i) key[i] = first[i];
         } else {
-            load(p, key);
-        }
-#pragma unroll
-        for (int i = 0; i < KPT; ++i)
-            if (p + i < body) count += key[i] > prefix ? 1ull : key[i] == prefix ? 1ull << 32 : 0ull;
-        uint64_t total;
-        uint64_t at = before + block_prefix(count, sums, total);
-        if (ctas > 1) {
-            if (tid == 0) s_total[0] = total;
-            cluster.sync();
-            uint64_t all = 0;
-            for (int r = 0; r < ctas; ++r) {
-                const uint64_t x = *cluster.map_shared_rank(&s_total[0], r);
-                if (r < rank) at += x;
-                all += x;
-            }
-            cluster.sync();
-            total = all;
-        }
-        before += total;
-        uint32_t above = (uint32_t)at, ties = (uint32_t)(at >> 32);
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) {
-            if (p + i >= body) break;
-            const bool gt = key[i] > prefix, eq = key[i] == prefix;
-            if (gt || (eq && ties < need)) {
-                const uint32_t to = above + (ties < need ? ties : need);
-                kept[to] = (int32_t)(p + i);
-                nw[to] = w[p + i];
-            }
-            above += gt;
-            ties += eq;
+            load(mine, first);
         }
     }
-    // the last positions, then what is left of the outputs
-    const int step = ctas * kSelectThreads, id = rank * kSelectThreads + tid;
+    // the outputs that do not depend on the selection: the last positions, and what is left over
+    const int step = ctas * THREADS, id = rank * THREADS + tid;
     for (int64_t p = (int64_t)body + id; p < n; p += step) {
         const int64_t to = (int64_t)want + (p - body);
         kept[to] = (int32_t)p;
         nw[to] = w[p];
     }
     for (int64_t i = (int64_t)m + id; i < a.keep; i += step) kept[i] = -1;
-    for (int64_t i = (int64_t)m + id; i < a.new_cap; i += step) nw[i] = 0.f;
-    if (ctas > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
+    {
+        // to the next 16 bytes one by one, then 4 at a time
+        const int64_t lead = m + ((4 - ((reinterpret_cast<uintptr_t>(nw + m) >> 2) & 3)) & 3);
+        const int64_t at4 = lead < a.new_cap ? lead : a.new_cap, end4 = at4 + (a.new_cap - at4) / 4 * 4;
+        for (int64_t i = (int64_t)m + id; i < at4; i += step) nw[i] = 0.f;
+        for (int64_t i = at4 + 4 * (int64_t)id; i < end4; i += 4 * (int64_t)step)
+            *reinterpret_cast<float4 *>(nw + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int64_t i = end4 + id; i < a.new_cap; i += step) nw[i] = 0.f;
+    }
+    if (!want) return;  // the same for the whole cluster
+    __syncthreads();
+
+    uint32_t prefix = 0, need = want;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        auto count = [&](uint32_t key) {
+            if (pass == 0 || (key >> (shift + bits)) == prefix >> (shift + bits))
+                atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1u)], 1u);
+        };
+        if constexpr (SHARED) {
+#pragma unroll 4
+            for (uint32_t c = tid; c < chunks; c += THREADS) {
+                const uint4 k = s_keys[c];
+                count(k.x), count(k.y), count(k.z), count(k.w);
+            }
+        } else {
+            uint32_t key[kKeys];
+            for (uint32_t p0 = mine; p0 < body; p0 += round) {
+                if (p0 == mine) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) key[i] = first[i];
+                } else {
+                    load(p0, key);
+                }
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i) count(key[i]);
+            }
+        }
+        if constexpr (CLUSTER)
+            cluster.sync();
+        else
+            __syncthreads();
+        // bins in descending order: thread t holds the BPT bins that end at kBins - 1 - BPT t
+        uint32_t c[BPT];
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) c[i] = 0;
+        const int low = kBins - BPT * (tid + 1);
+        for (int r = 0; r < ctas; ++r) {
+            const uint32_t *other = CLUSTER ? cluster.map_shared_rank(&hist[pass][0], r) : &hist[pass][0];
+#pragma unroll
+            for (int i = 0; i < BPT; i += 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(other + low + i);
+                c[i] += v.x, c[i + 1] += v.y;
+            }
+        }
+        uint32_t sum = 0, total;
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) sum += c[i];
+        uint32_t above = block_prefix<W>(sum, sums[pass], total);
+        if (tid == 0 && total < need) s_digit = 0, s_need = need;  // only if the weights changed meanwhile
+        if (above < need && need <= above + sum) {
+            int d = BPT - 1;
+#pragma unroll
+            for (int i = BPT - 1; i > 0; --i)
+                if (d == i && need > above + c[i]) above += c[i], d = i - 1;
+            s_digit = (uint32_t)(low + d);
+            s_need = need - above;
+        }
+        __syncthreads();
+        prefix |= s_digit << shift;
+        need = s_need;
+    }
+    // keys above `prefix` are kept, and the first `need` that equal it
+    if constexpr (SHARED) {
+        // each warp owns a stretch of positions, 32 adjacent ones per step: a count, the warps' prefix sums,
+        // then the places by ballots
+        const int lane = tid & 31, warp = tid >> 5;
+        const uint32_t *keys = reinterpret_cast<const uint32_t *>(s_keys);
+        const uint32_t words = chunks / 8, own = (words + W - 1) / W;
+        const uint32_t begin = min(warp * own, words), end = min(begin + own, words);
+        uint32_t gt = 0, eq = 0, total;
+        for (uint32_t i = begin; i < end; ++i) {
+            const uint32_t key = keys[32 * i + lane];
+            gt += key > prefix;
+            eq += key == prefix;
+        }
+        // below 65536 keys: 16-bit halves do not overflow
+        const uint32_t at = block_prefix<W>(gt | eq << 16, sums[3], total);
+        const uint32_t start = __shfl_sync(0xffffffffu, at, 0);
+        uint32_t above = start & 0xffffu, ties = start >> 16;
+        const uint32_t lower = (1u << lane) - 1u;
+        for (uint32_t i = begin; i < end; ++i) {
+            const uint32_t key = keys[32 * i + lane];
+            const unsigned some_gt = __ballot_sync(0xffffffffu, key > prefix);
+            const unsigned some_eq = __ballot_sync(0xffffffffu, key == prefix);
+            const uint32_t my_ties = ties + __popc(some_eq & lower);
+            const uint32_t to = above + __popc(some_gt & lower) + (my_ties < need ? my_ties : need);
+            // to < want always, unless the weights changed meanwhile
+            if ((key > prefix || (key == prefix && my_ties < need)) && to < want) {
+                const uint32_t p = 32 * i + lane;
+                kept[to] = (int32_t)p;
+                nw[to] = key_weight(key, w + p);
+            }
+            above += __popc(some_gt);
+            ties += __popc(some_eq);
+        }
+    } else {
+        uint32_t above0 = 0, ties0 = 0;  // in earlier rounds
+        for (uint32_t q = 0; q < body; q += round) {
+            const uint32_t p = q + mine;
+            uint32_t gt = 0, eq = 0;  // bit i: key i
+            {
+                uint32_t key[kKeys];
+                if (q == 0) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) key[i] = first[i];
+                } else {
+                    load(p, key);
+                }
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i) {
+                    gt |= key[i] > prefix ? 1u << i : 0u;
+                    eq |= key[i] == prefix ? 1u << i : 0u;
+                }
+            }
+            uint32_t total;
+            if (q) __syncthreads();  // the scratch is read by the last round
+            const uint32_t at = block_prefix<W>((uint32_t)__popc(gt) | (uint32_t)__popc(eq) << 16, sums[3], total);
+            uint32_t above = above0 + (at & 0xffffu), ties = ties0 + (at >> 16);
+            above0 += total & 0xffffu;
+            ties0 += total >> 16;
+            if constexpr (CLUSTER) {
+                if (tid == 0) s_total[0] = total;
+                cluster.sync();
+                for (int r = 0; r < ctas; ++r) {
+                    const uint32_t x = *cluster.map_shared_rank(&s_total[0], r);
+                    if (r < rank) above += x & 0xffffu, ties += x >> 16;
+                    if (r != rank) above0 += x & 0xffffu, ties0 += x >> 16;
+                }
+                cluster.sync();  // also: no CTA leaves while another reads its shared memory
+            }
+            for (uint32_t some = gt | eq; some; some &= some - 1) {
+                const int i = __ffs(some) - 1;
+                const bool is_eq = (eq >> i) & 1u;
+                if (!is_eq || ties < need) {
+                    const uint32_t to = above + (ties < need ? ties : need);
+                    if (to < want) {  // always, unless the weights changed meanwhile
+                        kept[to] = (int32_t)(p + i);
+                        nw[to] = __ldg(w + p + i);
+                    }
+                }
+                if (is_eq) ++ties; else ++above;
+            }
+        }
+    }
 }
 
 constexpr int kMoveRows = 64;  // kept rows a block moves at a time
 
+// Kept rows to their new places: one thread per row finds them, all threads copy.
 __global__ void __launch_bounds__(kCopyThreads) kv_move_kernel(const __grid_constant__ EvictArgs a, FastDiv chunks,
                                                                int64_t rows, int pieces) {
     __shared__ RowMove moves[kMoveRows];
@@ -447,11 +579,12 @@ int32_t kv_weights(const dcp::WeightsArgs &a, cudaStream_t stream) {
     return launch_status("dcp_kv_weights");
 }
 
-template <int KPT>
-cudaError_t launch_select(const dcp::EvictArgs &a, int ctas, cudaStream_t stream) {
+template <int THREADS, int STORE>
+cudaError_t launch_select(const dcp::EvictArgs &a, int ctas, size_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.src.heads * ctas));
-    cfg.blockDim = dim3(dcp::kSelectThreads);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -459,19 +592,28 @@ cudaError_t launch_select(const dcp::EvictArgs &a, int ctas, cudaStream_t stream
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dcp::kv_select_kernel<KPT>, a);
+    cfg.numAttrs = STORE == dcp::kCluster ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, dcp::kv_select_kernel<THREADS, STORE>, a);
 }
+
+constexpr int64_t kMaxShared = 49152;  // weights a CTA's shared memory holds (192 KB)
 
 int32_t kv_evict(const dcp::EvictArgs &a, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.B * a.src.heads;
-    // the longest row decides: 4 weights per thread of one CTA, else 16 and as many CTAs (at most
-    // 8, and at most what the grid's size allows) as hold it
-    const int64_t longest = a.cap < a.src.capacity ? a.cap : a.src.capacity;
-    int ctas = 1;
-    while (ctas < 8 && ctas * int64_t(16 * dcp::kSelectThreads) < longest && rows * ctas * 2 < (int64_t(1) << 31)) ctas *= 2;
-    const cudaError_t e = longest <= 4 * dcp::kSelectThreads ? launch_select<4>(a, 1, stream)
-                                                              : launch_select<16>(a, ctas, stream);
+    const int64_t longest = a.cap < a.src.capacity ? a.cap : a.src.capacity;  // the longest row there can be
+    cudaError_t e;
+    if (longest <= 256 * dcp::kKeys) {
+        e = launch_select<256, dcp::kRegisters>(a, 1, 0, stream);
+    } else if (longest <= kMaxShared) {
+        static InstanceCache cache;
+        if (!reserve_smem(dcp::kv_select_kernel<1024, dcp::kShared>, cache, kMaxShared * 4))
+            return fail(DCP_ERR_CUDA, "dcp_kv_evict: cannot reserve shared memory");
+        e = launch_select<1024, dcp::kShared>(a, 1, (size_t)((longest + 31) / 32 * 128), stream);
+    } else {
+        // as many CTAs (at most 8) as hold the row in registers, as far as the grid's size allows
+        int ctas = rows * 8 < (int64_t(1) << 31) ? 8 : 1;
+        e = launch_select<512, dcp::kCluster>(a, ctas, 0, stream);
+    }
     if (e != cudaSuccess) return launch_status("dcp_kv_evict");
     const int pieces = (a.keep - 1) / dcp::kMoveRows + 1;
     const int64_t blocks = rows * pieces;
