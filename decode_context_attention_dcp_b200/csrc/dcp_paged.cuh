@@ -74,6 +74,15 @@ __device__ __forceinline__ bool locate(const PagedCache &c, const int32_t *row, 
     return page >= 0 && page < c.num_pages;
 }
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 2^x, results below 2^-126 as 0 (a weight that small adds nothing to an fp32 sum near 1).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // ---- arguments --------------------------------------------------------------------------------
 struct AttentionArgs {
     PagedCache kv;

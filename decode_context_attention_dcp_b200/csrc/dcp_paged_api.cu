@@ -54,7 +54,8 @@ int32_t check_cache(const char *fn, const dcp_paged_kv *kv, bool used, dcp::Page
     if ((kv->head_dim * es) % 16 != 0)
         return fail(DCP_ERR_MISALIGNED, "%s: a row of %d elements is not a multiple of 16 bytes", fn,
                     (int)kv->head_dim);
-    if (kv->heads < 1) return fail(DCP_ERR_INVALID_ARG, "%s: key head count %d < 1", fn, (int)kv->heads);
+    if (kv->heads < 1 || kv->heads > DCP_MAX_PAGED_HEADS)
+        return fail(DCP_ERR_INVALID_ARG, "%s: key head count %d outside [1, %d]", fn, (int)kv->heads, DCP_MAX_PAGED_HEADS);
     if (kv->page_size < 1) return fail(DCP_ERR_INVALID_ARG, "%s: page size %d < 1", fn, (int)kv->page_size);
     if (kv->num_pages < 0 || kv->max_pages < 0) return fail(DCP_ERR_INVALID_ARG, "%s: negative page count", fn);
     if (kv->max_pages >= kLimit || kv->max_pages * kv->page_size >= kMaxPositions)

@@ -72,13 +72,6 @@ __device__ __forceinline__ void mma(Fp32, float *c, const uint32_t *a, uint32_t 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 2^x, results below 2^-126 as 0 (a weight that small adds nothing to an fp32 sum near 1).
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
 }
@@ -136,7 +129,6 @@ struct WeightShift<Fp16> {
     static constexpr float value = 8.f;
 };
 
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // ---- workspace --------------------------------------------------------------------------------

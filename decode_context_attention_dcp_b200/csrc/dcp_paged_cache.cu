@@ -20,6 +20,12 @@ struct RowMove {
     int64_t k_from, v_from, k_to, v_to;
 };
 
+// 16 bytes that this kernel reads once.
+__device__ __forceinline__ uint4 ld_once(const uint32_t *p) {
+    const Words<4> r = load_stream<4>(p);
+    return make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+}
+
 // Copies the rows listed in `moves` (in shared memory): 16-byte chunk c of row r by thread
 // (r * chunks + c) mod kCopyThreads, U chunks of K and of V in flight per thread.
 template <int U>
@@ -55,57 +61,44 @@ __device__ __forceinline__ void copy_rows(const RowMove *moves, int rows, FastDi
 }
 
 // ---- append -----------------------------------------------------------------------------------
-constexpr int kAppendRows = 64;  // rows a block places at a time
+constexpr int kAppendTokens = 32;  // tokens a block places at a time, at most
 
-// The last request that starts at or before token t, or -1: the 32 lanes probe 32 starts at once,
-// first those around the request that the token's share of all tokens points to (exact for plain
-// decode), then ever smaller ranges.  Reads stay inside qsl[0 .. num_reqs - 1].
+// The last request that starts at or before token t, or -1.  First the one that the token's share of
+// all tokens points to (exact for plain decode), else a binary search.  Reads stay inside
+// qsl[0 .. num_reqs].
 __device__ __forceinline__ int request_of(const AppendArgs &a, int t) {
-    const int lane = threadIdx.x & 31, R = a.num_reqs;
-    int lo = 0, hi = R;  // the answer + 1, the number of starts <= t, lies in [lo, hi]
-    int64_t guess = (int64_t)t * R / a.T - 15;
-    guess = guess < 0 ? 0 : guess;
-    {
-        const int64_t i = guess + lane;
-        const bool in = i < R;
-        const unsigned some = __ballot_sync(0xffffffffu, in);
-        const unsigned le = __ballot_sync(0xffffffffu, in && a.qsl[in ? i : 0] <= t);
-        // starts are non-decreasing: `le` is a prefix of `some`
-        const int n = __popc(le);
-        if (n) lo = (int)guess + n;
-        else hi = (int)guess;
-        if (n && n < __popc(some)) hi = lo;
+    int lo = 0, hi = a.num_reqs;  // the number of starts <= t lies in [lo, hi]
+    const int g = (int)((int64_t)t * a.num_reqs / a.T);
+    const int here = __ldg(a.qsl + g), next = __ldg(a.qsl + g + 1);
+    if (here > t) {
+        hi = g;
+    } else {
+        lo = g + 1;
+        if (next > t) hi = lo;
     }
-    for (int round = 0; round < 32 && lo < hi; ++round) {
-        const int64_t span = hi - lo;
-        const int64_t i = lo + (span * (lane + 1)) / 33;  // lo <= i < hi
-        const int n = __popc(__ballot_sync(0xffffffffu, a.qsl[i] <= t));
-        const int nlo = n == 0 ? lo : (int)(lo + (span * n) / 33) + 1;
-        hi = n == 32 ? hi : (int)(lo + (span * (n + 1)) / 33);
-        lo = nlo;
+    while (lo < hi) {
+        const int mid = lo + ((hi - lo) >> 1);
+        if (__ldg(a.qsl + mid) <= t) lo = mid + 1; else hi = mid;
     }
     return lo - 1;
 }
 
-// A block takes `per` tokens at a time (all heads, at most kAppendRows rows): each warp finds the
-// slots of its tokens, then the whole block copies the rows.
+// A block takes `per` <= 32 tokens at a time: lane i of its first warp finds the place of token i,
+// the tokens that this rank holds are put together, and the whole block copies their rows, all
+// heads, U chunks of K and of V in flight per thread.
 __global__ void __launch_bounds__(kCopyThreads) kv_append_kernel(const __grid_constant__ AppendArgs a, int per,
-                                                                 FastDiv chunks) {
-    __shared__ RowMove moves[kAppendRows];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int heads = a.kv.heads;
-    // rows of one token in pieces of at most kAppendRows heads
-    const int pieces = (heads - 1) / kAppendRows + 1;
-    const int64_t groups = ((int64_t)(a.T - 1) / per + 1) * pieces;
+                                                                 FastDiv chunks, FastDiv heads) {
+    constexpr int U = 4;
+    __shared__ RowMove moves[kAppendTokens];
+    __shared__ int s_tokens;
+    const int64_t groups = (int64_t)(a.T - 1) / per + 1;
     for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-        const int64_t tg = g / pieces;
-        const int h0 = (int)(g - tg * pieces) * kAppendRows, hn = min(heads - h0, kAppendRows);
-        const int t0 = (int)(tg * per), tn = (int)min((int64_t)per, (int64_t)a.T - t0);
-        for (int i = warp; i < tn; i += kCopyThreads / 32) {
-            const int t = t0 + i, r = request_of(a, t);
+        if (threadIdx.x < 32) {
+            const int64_t t = g * per + threadIdx.x;
+            const int r = (int)threadIdx.x < per && t < a.T ? request_of(a, (int)t) : -1;
             RowMove mv{-1, 0, 0, 0};
             if (r >= 0) {
-                const int64_t left = (int64_t)a.qsl[r + 1] - t, pos = (int64_t)a.seq_lens[r] - left;
+                const int64_t left = (int64_t)__ldg(a.qsl + r + 1) - t, pos = (int64_t)__ldg(a.seq_lens + r) - left;
                 bool mine = left > 0 && pos >= 0;
                 uint32_t p = (uint32_t)pos;
                 if (mine && !a.sh.one) {
@@ -123,30 +116,47 @@ __global__ void __launch_bounds__(kCopyThreads) kv_append_kernel(const __grid_co
                     mv.v_to = page * a.kv.v_page_w + slot * a.kv.v_slot_w;
                 }
             }
-            for (int h = lane; h < hn; h += 32) {
-                RowMove m = mv;
-                if (m.k_from >= 0) {
-                    m.k_from += (h0 + h) * a.k_sh_w;
-                    m.v_from += (h0 + h) * a.v_sh_w;
-                    m.k_to += (h0 + h) * a.kv.k_head_w;
-                    m.v_to += (h0 + h) * a.kv.v_head_w;
-                }
-                moves[i * hn + h] = m;
-            }
+            const unsigned held = __ballot_sync(0xffffffffu, mv.k_from >= 0);
+            if (mv.k_from >= 0) moves[__popc(held & ((1u << threadIdx.x) - 1u))] = mv;
+            if (threadIdx.x == 0) s_tokens = __popc(held);
         }
         __syncthreads();
-        copy_rows<4>(moves, tn * hn, chunks, a.k_new, a.v_new, a.kv.k, a.kv.v);
+        // item i: chunk c of head h of held token x, chunk fastest
+        const int64_t per_token = (int64_t)heads.d * chunks.d, items = s_tokens * per_token;
+        for (int64_t i0 = threadIdx.x; i0 < items; i0 += U * kCopyThreads) {
+            uint4 k[U], v[U];
+            uint32_t *k_to[U], *v_to[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t i = i0 + u * kCopyThreads;
+                if (i < items) {
+                    const uint32_t row = chunks.div((uint32_t)i), c = (uint32_t)i - row * chunks.d;
+                    const uint32_t x = heads.div(row), h = row - x * heads.d;
+                    const RowMove mv = moves[x];
+                    k[u] = ld_once(a.k_new + mv.k_from + h * a.k_sh_w + c * 4);
+                    v[u] = ld_once(a.v_new + mv.v_from + h * a.v_sh_w + c * 4);
+                    k_to[u] = a.kv.k + mv.k_to + h * a.kv.k_head_w + c * 4;
+                    v_to[u] = a.kv.v + mv.v_to + h * a.kv.v_head_w + c * 4;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * kCopyThreads < items) {
+                    *reinterpret_cast<uint4 *>(k_to[u]) = k[u];
+                    *reinterpret_cast<uint4 *>(v_to[u]) = v[u];
+                }
+        }
         __syncthreads();
     }
 }
 
 // ---- accumulated weights ----------------------------------------------------------------------
-constexpr int kWeighThreads = 256;
+constexpr int kWeighThreads = 128;
 
 // w[p] += sum_h exp(x[h][p] - l[h]): a block takes one row (request, key head) and every
-// `splits`-th stretch of 1024 of its positions; a thread owns 4 positions (adjacent ones and 16-byte
+// `splits`-th stretch of 512 of its positions; a thread owns 4 positions (adjacent ones and 16-byte
 // accesses where VEC, i.e. all rows start on 16 bytes).
-template <bool VEC>
+template <bool VEC, int U>
 __global__ void __launch_bounds__(kWeighThreads) kv_weights_kernel(const __grid_constant__ WeightsArgs a, int splits) {
     const int row = blockIdx.x / splits, part = blockIdx.x - row * splits;
     const int b = row / a.heads, j = row - b * a.heads;
@@ -167,22 +177,28 @@ __global__ void __launch_bounds__(kWeighThreads) kv_weights_kernel(const __grid_
 #pragma unroll
             for (int e = 0; e < 4; ++e) old[e] = p + e * STEP < n ? w[p + e * STEP] : 0.f;
         }
-#pragma unroll 4
-        for (int g = 0; g < a.group; ++g) {
-            const float l = l0[g * a.lse_sh];
-            const float *x = x0 + g * a.logits_sh + p;
-            float v[4];
-            if (VEC && whole) {
-                const float4 q = __ldcs(reinterpret_cast<const float4 *>(x));
-                v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-            } else {
+        for (int g0 = 0; g0 < a.group; g0 += U) {  // U heads' logits in flight
+            float l[U], v[U][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = p + e * STEP < n ? __ldcs(x + e * STEP) : 0.f;
+            for (int u = 0; u < U; ++u) {
+                const int g = min(g0 + u, a.group - 1);  // a head too many is read again and not added
+                const float *x = x0 + g * a.logits_sh + p;
+                l[u] = __ldg(l0 + g * a.lse_sh);
+                if (VEC && whole) {
+                    const float4 q = __ldcs(reinterpret_cast<const float4 *>(x));
+                    v[u][0] = q.x, v[u][1] = q.y, v[u][2] = q.z, v[u][3] = q.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[u][e] = p + e * STEP < n ? __ldcs(x + e * STEP) : 0.f;
+                }
             }
-            if (isfinite(l)) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    add[e] += a.base_e ? expf(v[e] - l) : exp2f(fmaf(v[e], 1.44269504088896340736f, -l));
+            for (int u = 0; u < U; ++u) {
+                if (g0 + u < a.group && isfinite(l[u])) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        add[e] += exp2_fast(a.base_e ? (v[u][e] - l[u]) * kLog2e : fmaf(v[u][e], kLog2e, -l[u]));
+                }
             }
         }
         if (VEC && whole) {
@@ -556,26 +572,26 @@ bool vector_rows(const void *p, int64_t s0, int64_t s1) {
 }  // namespace
 
 int32_t kv_append(const dcp::AppendArgs &a, cudaStream_t stream) {
-    // tokens per block: all of a block's rows at once, fewer where that would leave SMs without a block
-    const int64_t fit = clamp<int64_t>(dcp::kAppendRows / a.kv.heads, 1, 8);
-    const int64_t per = clamp<int64_t>(a.T / (2 * sm_count()), 1, fit);
-    const int64_t groups = (((int64_t)a.T - 1) / per + 1) * ((a.kv.heads - 1) / dcp::kAppendRows + 1);
+    // as many tokens per block as leave every SM eight blocks
+    const int64_t per = clamp<int64_t>(a.T / (8 * sm_count()), 1, dcp::kAppendTokens);
+    const int64_t groups = ((int64_t)a.T - 1) / per + 1;
     const int64_t grid = groups < 16 * sm_count() ? groups : 16 * sm_count();
-    dcp::kv_append_kernel<<<(unsigned)grid, dcp::kCopyThreads, 0, stream>>>(a, (int)per, divisor(a.kv.data_w / 4));
+    dcp::kv_append_kernel<<<(unsigned)grid, dcp::kCopyThreads, 0, stream>>>(a, (int)per, divisor(a.kv.data_w / 4),
+                                                                            divisor(a.kv.heads));
     return launch_status("dcp_kv_append");
 }
 
 int32_t kv_weights(const dcp::WeightsArgs &a, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.B * a.heads;
-    // blocks per row: one per 1024 positions, as long as that is not more than 16 waves
+    // blocks per row: one per 512 positions, as long as that is not more than 16 waves
     const int64_t stretches = ((int64_t)a.cap - 1) / (4 * dcp::kWeighThreads) + 1;
     const int64_t splits = clamp<int64_t>(16 * 8 * sm_count() / rows, 1, stretches);
     const bool vec = vector_rows(a.logits, a.logits_sb, a.logits_sh) && vector_rows(a.weights, a.w_sb, a.w_sh);
     const int64_t grid = rows * splits;  // below 2^31: rows is, and splits is 1 where rows is large
-    if (vec)
-        dcp::kv_weights_kernel<true><<<(unsigned)grid, dcp::kWeighThreads, 0, stream>>>(a, (int)splits);
-    else
-        dcp::kv_weights_kernel<false><<<(unsigned)grid, dcp::kWeighThreads, 0, stream>>>(a, (int)splits);
+    const bool few = a.group <= 4;
+    auto kernel = vec ? few ? dcp::kv_weights_kernel<true, 4> : dcp::kv_weights_kernel<true, 8>
+                      : few ? dcp::kv_weights_kernel<false, 4> : dcp::kv_weights_kernel<false, 8>;
+    kernel<<<(unsigned)grid, dcp::kWeighThreads, 0, stream>>>(a, (int)splits);
     return launch_status("dcp_kv_weights");
 }
 

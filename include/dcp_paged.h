@@ -49,6 +49,8 @@ extern "C" {
 
 /* Largest head_dim of the paged calls. */
 #define DCP_MAX_PAGED_DIM 256
+/* Largest number of key heads of a paged cache. */
+#define DCP_MAX_PAGED_HEADS (1 << 20)
 
 /*
  * A paged cache and the block table of the requests at hand.  Element d of key head h in slot
@@ -57,7 +59,7 @@ extern "C" {
  * interleaved pools are all described.
  *
  * Requirements: dtype a dcp_dtype; head_dim in [1, DCP_MAX_PAGED_DIM] with rows a multiple of
- * 16 bytes; heads >= 1; page_size >= 1; num_pages >= 0; max_pages >= 0; max_pages * page_size
+ * 16 bytes; heads in [1, DCP_MAX_PAGED_HEADS]; page_size >= 1; num_pages >= 0; max_pages >= 0; max_pages * page_size
  * < 2^31 - 1024; k and v 16-byte aligned; strides >= 0 and multiples of 16 bytes; block_table 4-byte
  * aligned, entry (b, j) at b*table_stride + j.
  */
