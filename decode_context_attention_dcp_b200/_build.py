@@ -1,10 +1,12 @@
-"""Build of libdcpcombine.so, in-tree, for sm_100a.
+"""Build of libdcpcombine.so, in-tree, for sm_100a, and of the paged calls' torch binding.
 
     python -m decode_context_attention_dcp_b200._build        # build if stale
     python -m decode_context_attention_dcp_b200._build --force
 
 nvcc cross-compiles without a GPU.  The library links the CUDA runtime
 statically, so it does not depend on which libcudart the host process loaded.
+The binding (_paged_binding.so) is host code: g++ against the headers of the
+Python and torch that import it.
 """
 from __future__ import annotations
 
@@ -15,6 +17,8 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +29,8 @@ LIBRARY = os.path.join(PKG, "libdcpcombine.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMPILE_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2"]
 LINK_FLAGS = ["-shared", "--cudart", "static"]
+BINDING_SOURCE = os.path.join(PKG, "binding", "paged_binding.cpp")
+BINDING = os.path.join(PKG, "_paged_binding.so")
 
 
 def nvcc() -> str:
@@ -69,7 +75,7 @@ def stale(lib: str = LIBRARY) -> bool:
 def _run(cmd: list[str]) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+        raise RuntimeError(os.path.basename(cmd[0]) + " failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -104,8 +110,54 @@ def build(force: bool = False, verbose: bool = False) -> str:
         shutil.rmtree(objdir, ignore_errors=True)
     return LIBRARY
 
+
+
+def binding_digest() -> str:
+    """SHA-256 of the binding's sources and of the Python and torch it is built for."""
+    import torch
+
+    h = hashlib.sha256()
+    h.update(f"{sys.version} {torch.__version__}".encode())
+    for p in (BINDING_SOURCE, *sorted(glob.glob(os.path.join(INCLUDE, "*.h")))):
+        with open(p, "rb") as fh:
+            h.update(b"\0" + fh.read())
+    return h.hexdigest()
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the torch binding of the paged calls (atomic replace)."""
+    import torch
+
+    digest = binding_digest()
+    if not force and os.path.exists(BINDING) and os.path.exists(_digest_file(BINDING)):
+        with open(_digest_file(BINDING)) as fh:
+            if fh.read().strip() == digest:
+                return BINDING
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
+    os.close(fd)
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include/torch/csrc/api/include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING_SOURCE,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-ldl",
+           "-o", tmp]
+    try:
+        _run(cmd)
+        os.replace(tmp, BINDING)
+        with open(_digest_file(BINDING) + ".tmp", "w") as fh:
+            fh.write(digest + "\n")
+        os.replace(_digest_file(BINDING) + ".tmp", _digest_file(BINDING))
+    finally:
+        if os.path.exists(tmp):
+            os.unlink(tmp)
+    return BINDING
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--force", action="store_true")
     args = ap.parse_args()
     print(build(force=args.force, verbose=True))
+    print(build_binding(force=args.force))

@@ -24,12 +24,14 @@ captured into a CUDA graph and replayed with other lengths.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
+import threading
 
 import torch
 
 # the package defines these before it imports this module
-from . import DCPError, _code, _cuda, _stream, dcp_last_error, dcp_lse_pack_dim, library
+from . import DCPError, _build, _code, _cuda, _stream, dcp_last_error, dcp_lse_pack_dim, library
 
 _i32, _i64, _ptr, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -61,6 +63,34 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.dcp_kv_weights.restype = _i32
     lib.dcp_kv_evict.argtypes = [kv, kv, _ptr, _ptr, _ptr, _ptr, _ptr, *[_i64] * 9, _i32, _i32, _i32, _ptr]
     lib.dcp_kv_evict.restype = _i32
+
+
+_native = None
+_lock = threading.Lock()
+
+
+def _binding():
+    """The compiled binding (built first if it is missing or older than its source).  Its functions
+    make the calls below in the usual case and return None in every other one, where the code here
+    makes the call or says what is wrong with it."""
+    global _native
+    if _native is None:
+        library()
+        with _lock:
+            if _native is None:
+                spec = importlib.util.spec_from_file_location(f"{__package__}._paged_binding", _build.build_binding())
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.set_library(_build.build())
+                _native = module
+    return _native
+
+
+def _done(status) -> bool:
+    """Whether the binding made the call; raises where the library refused it."""
+    if type(status) is int:
+        raise DCPError(status, dcp_last_error())
+    return status is not None
 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, requests: int,
@@ -195,6 +225,10 @@ def dcp_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     defaults to 1/sqrt(D).  logits [B, H, cap] fp32, if given, receives scale * (q . k_p) at the
     held positions p < cap.  workspace (paged_attention_workspace bytes) is allocated per call
     unless given; calls that may run at the same time need one each."""
+    if workspace is None and stream is None and _done(_binding().attend(
+            q, k_cache, v_cache, block_table, seq_lens, 0, scale, shard, num_shards, interleave, logits,
+            is_lse_base_on_e, result, lse)):
+        return
     B, H, D = q.shape
     if tuple(result.shape) != (B, H, D) or result.dtype != q.dtype or not result.is_contiguous():
         raise ValueError(f"result must be a contiguous [{B}, {H}, {D}] tensor of q's dtype")
@@ -211,6 +245,10 @@ def dcp_paged_attention_pack(q: torch.Tensor, k_cache: torch.Tensor, v_cache: to
                              workspace: torch.Tensor | None = None, stream=None) -> None:
     """dcp_paged_attention with its rows and LSEs written as dcp_pack would: send_buf [world_size, B,
     H/world_size, D + P]."""
+    if workspace is None and stream is None and world_size != 0 and _done(_binding().attend(
+            q, k_cache, v_cache, block_table, seq_lens, world_size, scale, shard, num_shards, interleave, logits,
+            is_lse_base_on_e, send_buf, None)):
+        return
     B, H, D = q.shape
     if world_size < 1 or H % world_size:
         raise ValueError(f"H={H} heads do not split over world_size={world_size}")
@@ -229,6 +267,9 @@ def dcp_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tenso
     Tokens query_start_loc[r] <= t < query_start_loc[r + 1] are the last ones of request r's
     seq_lens[r] positions (new tokens included).  Only the positions that this rank holds are
     written; tokens outside every request are skipped."""
+    if stream is None and _done(_binding().append(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
+                                                  query_start_loc, shard, num_shards, interleave)):
+        return
     dev = _cuda(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc)
     R = seq_lens.numel()
     _lens(seq_lens, R)
@@ -256,6 +297,9 @@ def dcp_kv_weights(logits: torch.Tensor, global_lse: torch.Tensor, seq_lens: tor
     [B, H, cap] - global_lse [B, H]) at the held positions, summed over the H / heads query heads of
     each key head.  global_lse is the LSE over all shards (the combine's); logits are
     paged_attention's."""
+    if stream is None and _done(_binding().weigh(logits, global_lse, seq_lens, weights, shard, num_shards, interleave,
+                                                 is_lse_base_on_e)):
+        return
     dev = _cuda(logits, global_lse, seq_lens, weights)
     if weights.dim() != 3 or logits.dim() != 3:
         raise ValueError("logits must be [B, H, cap] and weights [B, heads, cap]")
@@ -303,6 +347,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     interleave: int = 1, logits: torch.Tensor | None = None, is_lse_base_on_e: bool = True):
     """Attention of q [B, H, D] over this rank's shard: (result [B, H, D], lse [B, H] fp32), the
     partial pair that pack() or lse_weighted_combine() takes.  See dcp_paged_attention."""
+    out = _binding().attend(q, k_cache, v_cache, block_table, seq_lens, 0, scale, shard, num_shards, interleave, logits,
+                            is_lse_base_on_e, None, None)
+    if _done(out):
+        return out
     result = q.new_empty(q.shape)
     lse = q.new_empty(q.shape[:2], dtype=torch.float32)
     dcp_paged_attention(q, k_cache, v_cache, block_table, seq_lens, result, lse, scale, shard, num_shards, interleave,
@@ -316,6 +364,11 @@ def paged_attention_pack(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
                          is_lse_base_on_e: bool = True) -> torch.Tensor:
     """The packed send buffer [world_size, B, H/world_size, D + P] of paged_attention's result, in
     one step.  See dcp_paged_attention_pack."""
+    if world_size != 0:
+        out = _binding().attend(q, k_cache, v_cache, block_table, seq_lens, world_size, scale, shard, num_shards,
+                                interleave, logits, is_lse_base_on_e, None, None)
+        if _done(out):
+            return out
     B, H, D = q.shape
     if world_size < 1 or H % world_size:
         raise ValueError(f"H={H} heads do not split over world_size={world_size}")
@@ -336,11 +389,16 @@ def kv_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         raise DCPError(1, f"kv_evict: keep={keep} is less than 1")
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        k_out, v_out = k_cache, v_cache
+    out = _binding().evict(weights, k_cache, v_cache, block_table, seq_lens, k_out, v_out, new_block_table, keep, recent,
+                           shard, num_shards, interleave)
+    if _done(out):
+        return out
     B, heads, cap = weights.shape
     kept = weights.new_empty((B, heads, keep), dtype=torch.int32)
     new_lens = weights.new_empty(B, dtype=torch.int32)
     new_weights = weights.new_empty((B, heads, max(cap, keep)), dtype=torch.float32)
-    dcp_kv_evict(weights, k_cache, v_cache, block_table, seq_lens, k_cache if k_out is None else k_out,
-                 v_cache if v_out is None else v_out, new_block_table, keep, recent, kept, new_lens, new_weights,
-                 shard, num_shards, interleave)
+    dcp_kv_evict(weights, k_cache, v_cache, block_table, seq_lens, k_out, v_out, new_block_table, keep, recent, kept,
+                 new_lens, new_weights, shard, num_shards, interleave)
     return kept, new_lens, new_weights
