@@ -86,6 +86,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // ---- arguments --------------------------------------------------------------------------------
 struct AttentionArgs {
     PagedCache kv;
+    // The same strides in units of `unit` bytes (a power of two that divides them all): a row's offset
+    // in its pool then fits 32 bits (host-checked), and an address is one multiply-add.
+    uint32_t unit;
+    uint32_t k_page_u, k_slot_u, k_head_u;
+    uint32_t v_page_u, v_slot_u, v_head_u;
     Shards sh;
     const uint32_t *q;
     const int32_t *seq_lens;

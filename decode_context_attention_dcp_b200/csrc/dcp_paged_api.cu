@@ -105,6 +105,29 @@ int32_t check_shards(const char *fn, int32_t shard, int32_t num_shards, int32_t 
     return DCP_OK;
 }
 
+// The pools' strides in the largest unit (16 to 4096 bytes) that divides them; false where a row's
+// offset does not fit 32 bits.  Strides of dimensions of one entry do not matter.
+bool unit_strides(const dcp_paged_kv *kv, dcp::AttentionArgs &a) {
+    const int es = elem_size(kv->dtype);
+    const int64_t counts[3] = {kv->num_pages, kv->page_size, kv->heads};
+    const int64_t strides[6] = {kv->k_stride_page, kv->k_stride_slot, kv->k_stride_head,
+                                kv->v_stride_page, kv->v_stride_slot, kv->v_stride_head};
+    uint32_t *to[6] = {&a.k_page_u, &a.k_slot_u, &a.k_head_u, &a.v_page_u, &a.v_slot_u, &a.v_head_u};
+    a.unit = 4096;
+    for (int i = 0; i < 6; ++i)
+        while (counts[i % 3] > 1 && (strides[i] * es) % a.unit) a.unit >>= 1;
+    for (int pool = 0; pool < 2; ++pool) {
+        __int128 last = 0;
+        for (int i = 3 * pool; i < 3 * pool + 3; ++i) {
+            const __int128 u = counts[i % 3] > 1 ? (__int128)strides[i] * es / a.unit : 0;
+            last += u * (counts[i % 3] > 1 ? counts[i % 3] - 1 : 0);
+            *to[i] = (uint32_t)u;
+        }
+        if (last >> 32) return false;
+    }
+    return true;
+}
+
 // What both attention calls check and fill; result is `out` either way.
 int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const int32_t *seq_lens, void *out,
                   float *lse, float *logits, int64_t B, int64_t H, int32_t world_size, int64_t q_stride_b,
@@ -139,6 +162,9 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
     if (logits && (logits_cap < 0 || logits_cap >= kLimit))
         return fail(DCP_ERR_INVALID_ARG, "%s: logits_cap outside [0, 2^31)", fn);
     if (B == 0) return ok();
+    if (!unit_strides(kv, a))
+        return fail(DCP_ERR_INVALID_ARG, "%s: a pool spans more than 2^32 times %u bytes, the unit of its strides", fn,
+                    a.unit);
     if (!q || !seq_lens || !out || (!world_size && !lse))
         return fail(DCP_ERR_INVALID_ARG, "%s: null buffer pointer", fn);
     if (!aligned(q, 16) || !aligned(out, 16))

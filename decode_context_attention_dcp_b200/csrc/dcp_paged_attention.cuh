@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     __shared__ int s_where[3];
     __shared__ float2 s_stat[NW][S::kHeads];       // maximum and sum of each warp's heads at a merge
     __shared__ uint32_t s_held[ST][NW];            // bit r: position r of the warp's stage counts
-    __shared__ longlong2 s_row[NW][WP];            // addresses of the K and V rows being copied
+    __shared__ uint2 s_row[NW][WP];                // offsets of the K and V rows being copied
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");
 
@@ -345,6 +345,8 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     constexpr int kCopiesPerRow = S::kChunks > 32 ? S::kChunks / 32 : 1;
     const int my_row = S::kChunks > 32 ? 0 : lane / S::kChunks, my_chunk = S::kChunks > 32 ? lane : lane % S::kChunks;
     const uint32_t lane_to = my_row * S::kChunks * 16, lane_sw = (uint32_t)(my_chunk ^ my_row) << 4;
+    const char *const k_base = reinterpret_cast<const char *>(a.kv.k) + my_chunk * 16;
+    const char *const v_base = reinterpret_cast<const char *>(a.kv.v) + my_chunk * 16;
 
     // Starts the copies of the next tile (this warp's positions of it; the query with a new
     // request or head block) and moves on.
@@ -362,35 +364,35 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         }
         if (ld.t * TILE + warp * WP < ld.n) {
             const bool held = entry >= 0 && entry < a.kv.num_pages;
-            __syncwarp();  // the last tile's addresses have been read
-            if (lane < WP) {
-                longlong2 at;  // byte addresses of the rows' first chunks
-                at.x = reinterpret_cast<int64_t>(a.kv.k) +
-                       4 * (entry * a.kv.k_page_w + slot * a.kv.k_slot_w + ld.kvh * a.kv.k_head_w);
-                at.y = reinterpret_cast<int64_t>(a.kv.v) +
-                       4 * (entry * a.kv.v_page_w + slot * a.kv.v_slot_w + ld.kvh * a.kv.v_head_w);
-                s_row[warp][lane] = at;
-            }
+            __syncwarp();  // the last tile's offsets have been read
+            if (lane < WP)
+                s_row[warp][lane] = make_uint2(entry * a.k_page_u + slot * a.k_slot_u + ld.kvh * a.k_head_u,
+                                               entry * a.v_page_u + slot * a.v_slot_u + ld.kvh * a.v_head_u);
             const uint32_t bits = __ballot_sync(0xffffffffu, held) & ((1u << WP) - 1u);
             if (lane == 0) s_held[ld_stage][warp] = bits;
             __syncwarp();
             const uint32_t dst = stages + ld_stage * S::kStage + lane_to;
-            const bool all = bits == (1u << WP) - 1u && S::DP * S::kBytes == 4 * a.kv.data_w;
+            if (bits == (1u << WP) - 1u && S::DP * S::kBytes == 4 * a.kv.data_w) {
 #pragma unroll
-            for (int i = 0; i < WP * S::kChunks / 32; ++i) {
-                const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
-                const longlong2 at = s_row[warp][row0 + my_row];
-                // (row0 + my_row) mod 8 = (row0 mod 8) ^ my_row: my_row < kRowsPerCopy, which divides row0
-                const uint32_t to = dst + ((lane_sw ^ ((row0 & 7) << 4)) + (row0 * S::kChunks + c0) * 16);
-                const char *k = reinterpret_cast<const char *>(at.x) + (my_chunk + c0) * 16;
-                const char *v = reinterpret_cast<const char *>(at.y) + (my_chunk + c0) * 16;
-                if (all) {
-                    cp_async_16(to, k);
-                    cp_async_16(to + S::kHalf, v);
-                } else {
+                for (int i = 0; i < WP * S::kChunks / 32; ++i) {
+                    const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
+                    const uint2 at = s_row[warp][row0 + my_row];
+                    // (row0 + my_row) mod 8 = (row0 mod 8) ^ my_row: my_row < kRowsPerCopy, which divides row0
+                    const uint32_t to = dst + (lane_sw ^ ((row0 & 7) << 4));
+                    const int more = (row0 * S::kChunks + c0) * 16;
+                    cp_async_16(to + more, k_base + (uint64_t)at.x * a.unit + c0 * 16);
+                    cp_async_16(to + more + S::kHalf, v_base + (uint64_t)at.y * a.unit + c0 * 16);
+                }
+            } else {  // rows that are not held, or are shorter, are filled with zeros
+#pragma unroll 1
+                for (int i = 0; i < WP * S::kChunks / 32; ++i) {
+                    const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
+                    const uint2 at = s_row[warp][row0 + my_row];
+                    const uint32_t to = dst + (lane_sw ^ ((row0 & 7) << 4)) + (row0 * S::kChunks + c0) * 16;
                     const bool in = ((bits >> (row0 + my_row)) & 1u) && (my_chunk + c0) * 4 < a.kv.data_w;
-                    cp_async_or_zero(to, in ? (const void *)k : a.kv.k, in);
-                    cp_async_or_zero(to + S::kHalf, in ? (const void *)v : a.kv.v, in);
+                    cp_async_or_zero(to, in ? k_base + (uint64_t)at.x * a.unit + c0 * 16 : (const char *)a.kv.k, in);
+                    cp_async_or_zero(to + S::kHalf, in ? v_base + (uint64_t)at.y * a.unit + c0 * 16 : (const char *)a.kv.v,
+                                     in);
                 }
             }
         }

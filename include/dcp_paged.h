@@ -109,7 +109,9 @@ int64_t dcp_paged_attention_workspace(int64_t H, int32_t heads, int32_t head_dim
  *             initialisation and mean nothing afterwards.  Calls that may run at the same time
  *             need one each.
  *
- * Requirements: those of dcp_paged_kv; H a multiple of heads (else DCP_ERR_SHAPE); q and result
+ * Requirements: those of dcp_paged_kv, and no row of a pool further than 2^32 units from its start,
+ * a unit being the largest power of two up to 4096 bytes that divides all strides (64 GB for
+ * strides of odd multiples of 16 bytes); H a multiple of heads (else DCP_ERR_SHAPE); q and result
  * 16-byte aligned, q strides multiples of 16 bytes and >= 0; B*H < 2^31; shard in
  * [0, num_shards), num_shards in [1, DCP_MAX_SHARDS], interleave >= 1; scale finite.
  */
