@@ -59,6 +59,22 @@ int32_t launch_status(const char *what) {
     return ok();
 }
 
+// cuTensorMapEncodeTiled, found once through the runtime (the library does not link the driver).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+    static std::atomic<int> tried{0};
+    PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
+    if (f || tried.load(std::memory_order_acquire)) return f;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+        f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    fn.store(f, std::memory_order_release);
+    tried.store(1, std::memory_order_release);
+    return f;
+}
+
 }  // namespace dcp_host
 
 namespace {
@@ -71,6 +87,7 @@ using dcp_host::ok;
 using dcp_host::reserve_smem;
 using dcp_host::resident_ctas;
 using dcp_host::sm_count;
+using dcp_host::tensor_map_encoder;
 
 int elem_size(int32_t dtype) {
     switch (dtype) {
@@ -173,22 +190,6 @@ int32_t launch_pack(const char *fn, dcp::PackArgs a, const PackGeom &g, bool run
 }
 
 // ---- the tensor-copy pack (pack_tma_kernel) ----
-
-// cuTensorMapEncodeTiled, found once through the runtime (the library does not link the driver).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
-    static std::atomic<int> tried{0};
-    PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
-    if (f || tried.load(std::memory_order_acquire)) return f;
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-        f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    fn.store(f, std::memory_order_release);
-    tried.store(1, std::memory_order_release);
-    return f;
-}
 
 constexpr int kPackTmaStages = 2;
 constexpr int kPackTmaBoxBytes = 65536;  // about 64 KiB of rows per tile
@@ -331,6 +332,8 @@ int32_t dcp_wait_timeouts(uint64_t *count, int32_t reset) {
         const unsigned long long zero = 0;
         e = cudaMemcpyToSymbol(dcp::g_wait_timeouts, &zero, sizeof(zero));
     }
+    for (auto f : {dcp_host::attention_timeouts_bf16, dcp_host::attention_timeouts_fp16, dcp_host::attention_timeouts_fp32})
+        if (e == cudaSuccess) e = f(v, reset);
     if (e != cudaSuccess) return fail(DCP_ERR_CUDA, "dcp_wait_timeouts: %s", cudaGetErrorString(e));
     *count = v;
     return ok();

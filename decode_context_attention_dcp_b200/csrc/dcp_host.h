@@ -4,6 +4,8 @@
 // dispatchers (one translation unit each, so that they compile in parallel).
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -28,6 +30,16 @@ int32_t launch_status(const char *what);
 
 // Multiprocessor count of the current device (cached per device).
 int sm_count();
+
+// cuTensorMapEncodeTiled, found once through the runtime (the library does not link the driver);
+// null where the driver has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// Adds the timed-out waits of the paged attention kernels of one element type to `count`, and
+// clears them with reset != 0 (dcp_wait_timeouts).
+cudaError_t attention_timeouts_bf16(unsigned long long &count, int32_t reset);
+cudaError_t attention_timeouts_fp16(unsigned long long &count, int32_t reset);
+cudaError_t attention_timeouts_fp32(unsigned long long &count, int32_t reset);
 
 // Resident CTAs per SM of one kernel instance on the current device.
 template <class K>

@@ -20,8 +20,10 @@
 // attention_join_kernel merges them in share order (no atomics: the same bits every time).
 //
 // Inside a CTA each warp streams its own positions (warp w of NW takes every NW-th group of
-// 16) through its own ring of shared-memory stages with cp.async, and keeps its own softmax
-// state; warps meet only where a request begins (the query) and ends (the merge).
+// 16) through its own ring of shared-memory stages, and keeps its own softmax state; warps meet
+// only where a request begins (the query) and ends (the merge).  A stage is filled by tensor
+// copies (a box of 8 or 16 slots of one page, 128 bytes of each row) where the page size is a
+// multiple of 8, else row by row with cp.async.
 #pragma once
 
 #include "dcp_paged.cuh"
@@ -81,6 +83,16 @@ __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16u : 0u));
 }
 
+// A box of a 4-dimensional tensor map into shared memory, completing on `bar`.
+__device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // A float as two tf32 values: hi is x rounded to 10 fraction bits (half a step away from zero), lo
 // the rest (at most 2^-11 |x|), of which the product keeps 10 fraction bits: hi + lo = x to
 // 2^-21 |x|.
@@ -92,9 +104,13 @@ __device__ __forceinline__ void tf32_split(float x, uint32_t &hi, uint32_t &lo) 
 // ---- shapes -----------------------------------------------------------------------------------
 // T element type, DP head dim as laid out in shared memory (D <= DP, the rest zero), NH blocks of 8
 // query heads per pass over K and V, NW warps per CTA, ST stages per warp, CTAS resident CTAs per SM.
-template <class T_, int DP_, int NH_, int NW_, int ST_, int CTAS_>
+template <class T_, int DP_, int NH_, int NW_, int ST_, int CTAS_, int BOX_ = 0>
 struct AttentionShape {
     using T = T_;
+    // slots per tensor copy (16 or 8, which the page size is a multiple of), 0: cp.async
+    static constexpr int BOX = BOX_;
+    template <int BOX2>
+    using With = AttentionShape<T_, DP_, NH_, NW_, ST_, CTAS_, BOX2>;
     static constexpr int DP = DP_, NH = NH_, NW = NW_, ST = ST_, CTAS = CTAS_;
     static constexpr bool kHalfType = T::kPerWord == 2;
     static constexpr int kBytes = 4 / T::kPerWord;     // element size
@@ -102,6 +118,11 @@ struct AttentionShape {
     static constexpr int TILE = WP * NW;               // positions per CTA tile
     static constexpr int kHeads = 8 * NH;              // query heads per pass
     static constexpr int kChunks = DP * kBytes / 16;   // 16-byte chunks per row
+    // K and V of a stage lie in panels of 16 rows x 128 bytes, chunk c of row r of a panel at c ^ (r mod 8)
+    // (the tensor copies' 128-byte swizzle): the 8 rows of an ldmatrix, or of a fragment's float
+    // reads, fall into different banks
+    static constexpr int kPanels = DP * kBytes / 128;
+    static constexpr int kPanel = WP * 128;
     static constexpr int kHalf = WP * DP * kBytes;     // bytes of a stage's K (and of its V)
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kThreads = NW * 32;
@@ -251,8 +272,14 @@ __device__ __forceinline__ void write_result(const AttentionArgs &a, int b, int 
 __device__ __forceinline__ float finite_or_zero_max(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ---- the stream ---------------------------------------------------------------------------------
+// Tensor maps of the pools: [pages, slots, heads, D].
+struct PoolMaps {
+    CUtensorMap k, v;
+};
+
 template <class S>
-__global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(const __grid_constant__ AttentionArgs a) {
+__global__ void __launch_bounds__(S::kThreads, S::CTAS)
+    attention_stream_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ PoolMaps maps) {
     using T = typename S::T;
     constexpr int DP = S::DP, NH = S::NH, NW = S::NW, ST = S::ST, WP = S::WP, TILE = S::TILE;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -260,9 +287,15 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     __shared__ int s_where[3];
     __shared__ float2 s_stat[NW][S::kHeads];       // maximum and sum of each warp's heads at a merge
     __shared__ uint32_t s_held[ST][NW];            // bit r: position r of the warp's stage counts
-    __shared__ uint2 s_row[NW][WP];                // offsets of the K and V rows being copied
+    __shared__ uint2 s_row[NW][WP];                // cp.async: offsets of the K and V rows being copied
+    __shared__ uint64_t s_full[NW][ST];            // tensor copies: a stage's bytes have arrived
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");
+    constexpr bool TENSOR = S::BOX > 0;
+    if (TENSOR && lane == 0) {
+        for (int st = 0; st < ST; ++st) mbar_init(&s_full[warp][st], 1);
+        mbar_fence_init();
+    }
 
     // the share: all lengths summed in one block scan, then the request where it begins
     int64_t begin, count;
@@ -323,11 +356,16 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     const uint32_t queries = smem_addr(smem) + NW * ST * S::kStage;
     uint2 *const query_pairs = reinterpret_cast<uint2 *>(smem + NW * ST * S::kStage);  // fp32
 
-    // This lane's row of the tile that is copied next: its page is read one tile ahead.
+    // What this lane copies of a tile: cp.async, row lane mod 16; tensor copies, box `lane` of kBoxes (K's
+    // then V's, row groups of BOX slots, panels).  Its page is read one tile ahead.
+    constexpr int kGroups = TENSOR ? WP / (TENSOR ? S::BOX : 1) : 1, kBoxes = 2 * kGroups * S::kPanels;
+    static_assert(kBoxes <= 32, "one box per lane");
+    const int box_panel = lane % S::kPanels, box_group = lane / S::kPanels % kGroups;
+    const int my_first = TENSOR ? box_group * S::BOX : lane & (WP - 1);
     int entry = -1;
     uint32_t slot = 0;
     auto next_page = [&]() {
-        const int p = ld.t * TILE + warp * WP + (lane & (WP - 1));
+        const int p = ld.t * TILE + warp * WP + my_first;
         entry = -1;
         if (p < ld.n) {
             const uint32_t j = a.kv.page.div((uint32_t)p);
@@ -338,13 +376,12 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     next_page();
     int ld_query = 0, ld_stage = 0;
 
-    // One warp-wide copy covers kRowsPerCopy rows (or a 32-chunk part of one).  Chunk c of row r lies
-    // at chunk c ^ (r mod 8) of its row in shared memory, so that the 8 rows of an ldmatrix, or
-    // of a fragment's float reads, fall into different banks.
+    // cp.async: one warp-wide copy covers kRowsPerCopy rows (or a 32-chunk part of one)
     constexpr int kRowsPerCopy = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;
     constexpr int kCopiesPerRow = S::kChunks > 32 ? S::kChunks / 32 : 1;
     const int my_row = S::kChunks > 32 ? 0 : lane / S::kChunks, my_chunk = S::kChunks > 32 ? lane : lane % S::kChunks;
-    const uint32_t lane_to = my_row * S::kChunks * 16, lane_sw = (uint32_t)(my_chunk ^ my_row) << 4;
+    const uint32_t lane_to = (my_chunk >> 3) * S::kPanel + my_row * 128;
+    const uint32_t lane_sw = (uint32_t)((my_chunk & 7) ^ my_row) << 4;
     const char *const k_base = reinterpret_cast<const char *>(a.kv.k) + my_chunk * 16;
     const char *const v_base = reinterpret_cast<const char *>(a.kv.v) + my_chunk * 16;
 
@@ -362,37 +399,60 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
             }
             ld_query = ld_query + 1 == ST ? 0 : ld_query + 1;
         }
-        if (ld.t * TILE + warp * WP < ld.n) {
+        const int p0 = ld.t * TILE + warp * WP;
+        if (p0 < ld.n) {
             const bool held = entry >= 0 && entry < a.kv.num_pages;
-            __syncwarp();  // the last tile's offsets have been read
-            if (lane < WP)
-                s_row[warp][lane] = make_uint2(entry * a.k_page_u + slot * a.k_slot_u + ld.kvh * a.k_head_u,
-                                               entry * a.v_page_u + slot * a.v_slot_u + ld.kvh * a.v_head_u);
-            const uint32_t bits = __ballot_sync(0xffffffffu, held) & ((1u << WP) - 1u);
-            if (lane == 0) s_held[ld_stage][warp] = bits;
-            __syncwarp();
-            const uint32_t dst = stages + ld_stage * S::kStage + lane_to;
-            if (bits == (1u << WP) - 1u && S::DP * S::kBytes == 4 * a.kv.data_w) {
+            const uint32_t votes = __ballot_sync(0xffffffffu, held);
+            if constexpr (TENSOR) {
+                const int left = ld.n - p0;
+                uint32_t bits = left < WP ? (1u << left) - 1u : (1u << WP) - 1u;
 #pragma unroll
-                for (int i = 0; i < WP * S::kChunks / 32; ++i) {
-                    const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
-                    const uint2 at = s_row[warp][row0 + my_row];
-                    // (row0 + my_row) mod 8 = (row0 mod 8) ^ my_row: my_row < kRowsPerCopy, which divides row0
-                    const uint32_t to = dst + (lane_sw ^ ((row0 & 7) << 4));
-                    const int more = (row0 * S::kChunks + c0) * 16;
-                    cp_async_16(to + more, k_base + (uint64_t)at.x * a.unit + c0 * 16);
-                    cp_async_16(to + more + S::kHalf, v_base + (uint64_t)at.y * a.unit + c0 * 16);
+                for (int r = 0; r < kGroups; ++r)
+                    if (!((votes >> (r * S::kPanels)) & 1u)) bits &= ~(((1u << S::BOX) - 1u) << (r * S::BOX));
+                if (lane == 0) {
+                    s_held[ld_stage][warp] = bits;
+                    mbar_arrive_expect_tx(&s_full[warp][ld_stage], S::kStage);
                 }
-            } else {  // rows that are not held, or are shorter, are filled with zeros
+                __syncwarp();
+                // a page outside the pool, or past the length (-1), reads zeros
+                if (lane < kBoxes) {
+                    const bool is_v = lane >= kBoxes / 2;
+                    tensor_copy(stages + ld_stage * S::kStage + (is_v ? S::kHalf : 0) + box_panel * S::kPanel +
+                                    box_group * (S::BOX * 128),
+                                is_v ? &maps.v : &maps.k, box_panel * (128 / S::kBytes), ld.kvh,
+                                entry < 0 ? 0 : (int)slot, entry, &s_full[warp][ld_stage]);
+                }
+            } else {
+                const uint32_t bits = votes & ((1u << WP) - 1u);
+                __syncwarp();  // the last tile's offsets have been read
+                if (lane < WP)
+                    s_row[warp][lane] = make_uint2(entry * a.k_page_u + slot * a.k_slot_u + ld.kvh * a.k_head_u,
+                                                   entry * a.v_page_u + slot * a.v_slot_u + ld.kvh * a.v_head_u);
+                if (lane == 0) s_held[ld_stage][warp] = bits;
+                __syncwarp();
+                const uint32_t dst = stages + ld_stage * S::kStage + lane_to;
+                if (bits == (1u << WP) - 1u && S::DP * S::kBytes == 4 * a.kv.data_w) {
+#pragma unroll
+                    for (int i = 0; i < WP * S::kChunks / 32; ++i) {
+                        const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
+                        const uint2 at = s_row[warp][row0 + my_row];
+                        // (row0 + my_row) mod 8 = (row0 mod 8) ^ my_row: my_row < kRowsPerCopy, which divides row0
+                        const uint32_t to = dst + (lane_sw ^ ((row0 & 7) << 4));
+                        const int more = row0 * 128 + c0 / 8 * S::kPanel;
+                        cp_async_16(to + more, k_base + (uint64_t)at.x * a.unit + c0 * 16);
+                        cp_async_16(to + more + S::kHalf, v_base + (uint64_t)at.y * a.unit + c0 * 16);
+                    }
+                } else {  // rows that are not held, or are shorter, are filled with zeros
 #pragma unroll 1
-                for (int i = 0; i < WP * S::kChunks / 32; ++i) {
-                    const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
-                    const uint2 at = s_row[warp][row0 + my_row];
-                    const uint32_t to = dst + (lane_sw ^ ((row0 & 7) << 4)) + (row0 * S::kChunks + c0) * 16;
-                    const bool in = ((bits >> (row0 + my_row)) & 1u) && (my_chunk + c0) * 4 < a.kv.data_w;
-                    cp_async_or_zero(to, in ? k_base + (uint64_t)at.x * a.unit + c0 * 16 : (const char *)a.kv.k, in);
-                    cp_async_or_zero(to + S::kHalf, in ? v_base + (uint64_t)at.y * a.unit + c0 * 16 : (const char *)a.kv.v,
-                                     in);
+                    for (int i = 0; i < WP * S::kChunks / 32; ++i) {
+                        const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
+                        const uint2 at = s_row[warp][row0 + my_row];
+                        const uint32_t to = dst + (lane_sw ^ ((row0 & 7) << 4)) + row0 * 128 + c0 / 8 * S::kPanel;
+                        const bool in = ((bits >> (row0 + my_row)) & 1u) && (my_chunk + c0) * 4 < a.kv.data_w;
+                        cp_async_or_zero(to, in ? k_base + (uint64_t)at.x * a.unit + c0 * 16 : (const char *)a.kv.k, in);
+                        cp_async_or_zero(to + S::kHalf,
+                                         in ? v_base + (uint64_t)at.y * a.unit + c0 * 16 : (const char *)a.kv.v, in);
+                    }
                 }
             }
         }
@@ -417,20 +477,21 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
     uint32_t qf[S::kQueryRegs ? NH : 1][S::kQueryRegs ? DP * S::kBytes / 32 : 1][S::kHalfType ? 2 : 4];
     int cp_query = 0, cp_stage = 0, first_t = cp.t;
     uint32_t query = queries;
-    // Places of this lane in a stage: ldmatrix rows of K (16-bit) or its floats of K (fp32), and of V.
-    // Chunk c of row r lies at c ^ (r mod 8): of c = 2 j + e the part that depends on j mod 4 is in
-    // these, the rest is a constant 128 (j / 4).
+    // Places of this lane in a stage: ldmatrix rows of K (16-bit) or its floats of K (fp32), and of V.  Of
+    // chunk c = 2 j + e the part that depends on j mod 4 is in these, the rest is panel j / 4.
+    uint32_t phases = 0;   // bit st: parity of stage st's next arrival
+    bool late = false;     // a wait ran out: nothing more is waited for, the result is not valid
     uint32_t k_at[4], v_at[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if constexpr (S::kHalfType) {
             const int rk = lane & 15, rv = (lane & 7) + ((lane >> 4) << 3);
-            k_at[j] = rk * (DP * 2) + (((2 * j + (lane >> 4)) ^ (rk & 7)) << 4);
-            v_at[j] = S::kHalf + rv * (DP * 2) + (((2 * j + ((lane >> 3) & 1)) ^ (rv & 7)) << 4);
+            k_at[j] = rk * 128 + (((2 * j + (lane >> 4)) ^ (rk & 7)) << 4);
+            v_at[j] = S::kHalf + rv * 128 + (((2 * j + ((lane >> 3) & 1)) ^ (rv & 7)) << 4);
         } else {
-            k_at[j] = g * (DP * 4) + (((2 * j) ^ g) << 4) + t4 * 4;
+            k_at[j] = g * 128 + (((2 * j) ^ g) << 4) + t4 * 4;
             // position 2 t4 (the next one's chunks differ in bit 0), column 8 j + g
-            v_at[j] = S::kHalf + 2 * t4 * (DP * 4) + (((2 * j + (g >> 2)) ^ (2 * t4)) << 4) + (g & 3) * 4;
+            v_at[j] = S::kHalf + 2 * t4 * 128 + (((2 * j + (g >> 2)) ^ (2 * t4)) << 4) + (g & 3) * 4;
         }
     }
 
@@ -504,6 +565,24 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         if (p0 < cp.n) {
             const uint32_t stage = stages + cp_stage * S::kStage;
             const uint32_t held = s_held[cp_stage][warp];
+            if constexpr (TENSOR) {
+                if (!late && !mbar_wait_bounded(&s_full[warp][cp_stage], (phases >> cp_stage) & 1u, kWaitLimitNs)) {
+                    late = true;
+                    if (lane == 0) atomicAdd(&g_wait_timeouts, 1ull);
+                }
+                phases ^= 1u << cp_stage;
+                if (held != (1u << WP) - 1u) {
+                    // slots past the length hold anything; a weight of 0 must find a finite value there
+                    for (int x = lane; x < WP * S::kChunks; x += 32) {
+                        const int r = x / S::kChunks, c = x - r * S::kChunks;
+                        if (!((held >> r) & 1u))
+                            *reinterpret_cast<uint4 *>(smem + (stage - smem_addr(smem)) + S::kHalf + (c >> 3) * S::kPanel +
+                                                       r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async();  // before the stage's next tensor copy
+                    __syncwarp();
+                }
+            }
             const bool held0 = (held >> g) & 1u, held1 = (held >> (g + 8)) & 1u;
             // ---- x = K q^T: x[h][0, 1] position g and heads 2 t4, 2 t4 + 1; x[h][2, 3] position g + 8
             float x[NH][4];
@@ -516,8 +595,8 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ks += 2) {
                     uint32_t k0[4], k1[4];
-                    ldmatrix4(k0, stage + k_at[ks & 3] + (ks >> 2) * 128);
-                    ldmatrix4(k1, stage + k_at[(ks + 1) & 3] + (ks >> 2) * 128);
+                    ldmatrix4(k0, stage + k_at[ks & 3] + (ks >> 2) * S::kPanel);
+                    ldmatrix4(k1, stage + k_at[(ks + 1) & 3] + (ks >> 2) * S::kPanel);
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
                         uint32_t q[4];
@@ -544,12 +623,12 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                     for (int e = 0; e < 4; ++e) x[h][e] = x1[h][e] = x2[h][e] = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < DP / 8; ++ks) {
-                    const uint32_t at = stage - smem_addr(smem) + k_at[ks & 3] + (ks >> 2) * 128, next = at ^ 16;
+                    const uint32_t at = stage - smem_addr(smem) + k_at[ks & 3] + (ks >> 2) * S::kPanel, next = at ^ 16;
                     uint32_t kh[4], kl[4];
                     tf32_split(*reinterpret_cast<const float *>(smem + at), kh[0], kl[0]);
-                    tf32_split(*reinterpret_cast<const float *>(smem + at + 8 * DP * 4), kh[1], kl[1]);
+                    tf32_split(*reinterpret_cast<const float *>(smem + at + 8 * 128), kh[1], kl[1]);
                     tf32_split(*reinterpret_cast<const float *>(smem + next), kh[2], kl[2]);
-                    tf32_split(*reinterpret_cast<const float *>(smem + next + 8 * DP * 4), kh[3], kl[3]);
+                    tf32_split(*reinterpret_cast<const float *>(smem + next + 8 * 128), kh[3], kl[3]);
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
                         uint32_t q[4];
@@ -649,7 +728,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
 #pragma unroll
                 for (int j = 0; j < DP / 16; ++j) {
                     uint32_t v[4];
-                    ldmatrix4_trans(v, stage + v_at[j & 3] + (j >> 2) * 128);
+                    ldmatrix4_trans(v, stage + v_at[j & 3] + (j >> 2) * S::kPanel);
 #pragma unroll
                     for (int h = 0; h < NH; ++h) mma(T{}, o[h][j], v, hi[h][0], hi[h][1]);
 #pragma unroll
@@ -676,13 +755,13 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                     for (int j = 0; j < DP / 16; ++j) {
                         // columns 16 j + g and, 2 chunks on, 16 j + 8 + g; position 2 t4 + 1 is a row on, its chunks
                         // differ in bit 0
-                        const uint32_t base = stage - smem_addr(smem) + f * (8 * DP * 4) + (j >> 1) * 128;
+                        const uint32_t base = stage - smem_addr(smem) + f * (8 * 128) + (j >> 1) * S::kPanel;
                         const uint32_t c0 = base + v_at[(2 * j) & 3], c1 = base + v_at[(2 * j + 1) & 3];
                         uint32_t vh[4], vl[4];
                         tf32_split(*reinterpret_cast<const float *>(smem + c0), vh[0], vl[0]);
                         tf32_split(*reinterpret_cast<const float *>(smem + c1), vh[1], vl[1]);
-                        tf32_split(*reinterpret_cast<const float *>(smem + (c0 ^ 16) + DP * 4), vh[2], vl[2]);
-                        tf32_split(*reinterpret_cast<const float *>(smem + (c1 ^ 16) + DP * 4), vh[3], vl[3]);
+                        tf32_split(*reinterpret_cast<const float *>(smem + (c0 ^ 16) + 128), vh[2], vl[2]);
+                        tf32_split(*reinterpret_cast<const float *>(smem + (c1 ^ 16) + 128), vh[3], vl[3]);
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
                             mma(T{}, o[h][j], vh, wh[h][f][0], wh[h][f][1]);
@@ -756,6 +835,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
                 }
                 __syncthreads();
             }
+            if (TENSOR) fence_proxy_async();  // the rows written above, before the stage's next tensor copy
             if (i + 1 == count && tid == 0) {
                 int4 spill = make_int4(0, cp.b, cp.kvh, cp.rb);
                 // parts: this share and those up to the one with the request's last tile
@@ -766,6 +846,11 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS) attention_stream_kernel(
         }
         cp_stage = cp_stage + 1 == ST ? 0 : cp_stage + 1;
         iter_next<TILE>(a, cp);
+    }
+    if (TENSOR && late) {  // copies may still be on their way into this CTA's shared memory: wait, bounded
+        const uint64_t t0 = global_ns();
+        for (uint32_t spin = 0; spin < (1u << 26) && global_ns() - t0 < kWaitLimitNs; ++spin) {
+        }
     }
 }
 
@@ -913,7 +998,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
 namespace dcp_host {
 
 template <class S>
-int32_t launch_attention(dcp::AttentionArgs a, cudaStream_t stream) {
+int32_t launch_stream(dcp::AttentionArgs a, const dcp::PoolMaps &maps, cudaStream_t stream) {
     using T = typename S::T;
     static InstanceCache cache;
     const char *fn = "dcp_paged_attention";
@@ -924,7 +1009,7 @@ int32_t launch_attention(dcp::AttentionArgs a, cudaStream_t stream) {
     const int64_t most = (int64_t)sm_count() * S::CTAS;
     const int64_t tiles = (int64_t)a.B * a.head_blocks * (a.kv.capacity / S::TILE + 1);
     const int grid = (int)(tiles < most ? tiles : most);
-    dcp::attention_stream_kernel<S><<<grid, S::kThreads, S::kSmem, stream>>>(a);
+    dcp::attention_stream_kernel<S><<<grid, S::kThreads, S::kSmem, stream>>>(a, maps);
     int32_t st = launch_status(fn);
     if (st != DCP_OK) return st;
     // the join's launch overlaps the stream's end; its blocks wait for it before they read
@@ -943,15 +1028,46 @@ int32_t launch_attention(dcp::AttentionArgs a, cudaStream_t stream) {
     return launch_status(fn);
 }
 
+// The tensor map of a pool, boxes of `box` slots x 128 bytes of one head's rows; false where the
+// driver refuses it.
+inline bool pool_map(CUtensorMap &map, const void *base, const dcp::PagedCache &c, int64_t page_w, int64_t slot_w,
+                     int64_t head_w, int es, int box) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode || c.num_pages < 1) return false;
+    const cuuint64_t dim[4] = {(cuuint64_t)c.data_w * 4 / es, (cuuint64_t)c.heads, (cuuint64_t)c.page.d,
+                               (cuuint64_t)(c.num_pages < INT32_MAX ? c.num_pages : INT32_MAX)};
+    // a dimension of one entry takes any stride
+    const int64_t w[3] = {head_w, slot_w, page_w};
+    cuuint64_t stride[3];
+    for (int i = 0; i < 3; ++i) stride[i] = dim[i + 1] > 1 ? (cuuint64_t)w[i] * 4 : (cuuint64_t)c.data_w * 4;
+    const cuuint32_t boxes[4] = {(cuuint32_t)(128 / es), 1, (cuuint32_t)box, 1}, one[4] = {1, 1, 1, 1};
+    return encode(&map, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
+                  const_cast<void *>(base), dim, stride, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B,
+                  c.data_w >= 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class S>
+int32_t launch_attention(const dcp::AttentionArgs &a, cudaStream_t stream) {
+    dcp::PoolMaps maps;
+    const int box = a.kv.page.d % 16 == 0 ? 16 : a.kv.page.d % 8 == 0 ? 8 : 0;
+    if (box && pool_map(maps.k, a.kv.k, a.kv, a.kv.k_page_w, a.kv.k_slot_w, a.kv.k_head_w, S::kBytes, box) &&
+        pool_map(maps.v, a.kv.v, a.kv, a.kv.v_page_w, a.kv.v_slot_w, a.kv.v_head_w, S::kBytes, box))
+        return box == 16 ? launch_stream<typename S::template With<16>>(a, maps, stream)
+                         : launch_stream<typename S::template With<8>>(a, maps, stream);
+    return launch_stream<S>(a, maps, stream);
+}
+
 // The shape for a group of G query heads per key head and D elements.
 template <class T, class F>
 auto with_shape(int32_t group, int32_t head_dim, F &&f) {
     using dcp::AttentionShape;
     if constexpr (T::kPerWord == 2) {
         if (head_dim <= 64)
-            return group <= 8    ? f(AttentionShape<T, 64, 1, 4, 3, 4>{})
-                   : group <= 16 ? f(AttentionShape<T, 64, 2, 4, 3, 4>{})
-                                 : f(AttentionShape<T, 64, 4, 4, 3, 3>{});
+            return group <= 8    ? f(AttentionShape<T, 64, 1, 4, 6, 2>{})
+                   : group <= 16 ? f(AttentionShape<T, 64, 2, 4, 6, 2>{})
+                                 : f(AttentionShape<T, 64, 4, 4, 4, 2>{});
         if (head_dim <= 128)
             return group <= 8    ? f(AttentionShape<T, 128, 1, 4, 2, 3>{})
                    : group <= 16 ? f(AttentionShape<T, 128, 2, 4, 2, 3>{})
@@ -971,6 +1087,17 @@ int32_t paged_attention(const dcp::AttentionArgs &a, cudaStream_t stream) {
     return with_shape<T>(a.group, (int32_t)(a.kv.data_w * T::kPerWord), [&](auto shape) {
         return launch_attention<decltype(shape)>(a, stream);
     });
+}
+
+inline cudaError_t attention_timeouts(unsigned long long &count, int32_t reset) {
+    unsigned long long v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, dcp::g_wait_timeouts, sizeof(v));
+    if (e == cudaSuccess && reset) {
+        const unsigned long long zero = 0;
+        e = cudaMemcpyToSymbol(dcp::g_wait_timeouts, &zero, sizeof(zero));
+    }
+    count += v;
+    return e;
 }
 
 template <class T>

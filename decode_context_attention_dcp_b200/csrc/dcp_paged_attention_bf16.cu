@@ -11,4 +11,8 @@ int64_t attention_workspace_bf16(int32_t group, int32_t head_dim) {
     return attention_workspace<dcp::Bf16>(group, head_dim);
 }
 
+cudaError_t attention_timeouts_bf16(unsigned long long &count, int32_t reset) {
+    return attention_timeouts(count, reset);
+}
+
 }  // namespace dcp_host
