@@ -616,13 +616,20 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                     for (int e = 0; e < 4; ++e) x[h][e] += x1[h][e];
             } else {
                 // three tf32 products: hi hi + hi lo + lo hi (lo lo is below 2^-22 of the product)
-                float x1[NH][4], x2[NH][4];
+                // hi hi in sums of 16 elements, added in fp32: the product units cut what they add to a sum
+                float x1[NH][4], x2[NH][4], part[NH][4];
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[h][e] = x1[h][e] = x2[h][e] = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < DP / 8; ++ks) {
+                    if (ks % 2 == 0) {
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) part[h][e] = 0.f;
+                    }
                     const uint32_t at = stage - smem_addr(smem) + k_at[ks & 3] + (ks >> 2) * S::kPanel, next = at ^ 16;
                     uint32_t kh[4], kl[4];
                     tf32_split(*reinterpret_cast<const float *>(smem + at), kh[0], kl[0]);
@@ -640,9 +647,15 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                             const uint2 q0 = qp[((2 * ks) ^ g) * 4], q1 = qp[((2 * ks + 1) ^ g) * 4];
                             q[0] = q0.x, q[1] = q1.x, q[2] = q0.y, q[3] = q1.y;
                         }
-                        mma(T{}, x[h], kh, q[0], q[1]);
+                        mma(T{}, part[h], kh, q[0], q[1]);
                         mma(T{}, x1[h], kh, q[2], q[3]);
                         mma(T{}, x2[h], kl, q[0], q[1]);
+                    }
+                    if (ks % 2 == 1) {
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[h][e] += part[h][e];
                     }
                 }
 #pragma unroll
@@ -749,10 +762,17 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                             const float odd = __shfl_sync(0xffffffffu, w[h][2 * f + 1], from);
                             tf32_split(g & 1 ? odd : even, wh[h][f][e], wl[h][f][e]);
                         }
+// the tile's products in sums of their own, added to o in fp32: the product units cut what they
+                // add to a long sum, which over thousands of positions would be seen (1.6e-6 of the result)
 #pragma unroll
-                for (int f = 0; f < 2; ++f)
+                for (int j = 0; j < DP / 16; ++j) {
+                    float tile[NH][4];
 #pragma unroll
-                    for (int j = 0; j < DP / 16; ++j) {
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tile[h][e] = 0.f;
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
                         // columns 16 j + g and, 2 chunks on, 16 j + 8 + g; position 2 t4 + 1 is a row on, its chunks
                         // differ in bit 0
                         const uint32_t base = stage - smem_addr(smem) + f * (8 * 128) + (j >> 1) * S::kPanel;
@@ -764,11 +784,16 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                         tf32_split(*reinterpret_cast<const float *>(smem + (c1 ^ 16) + 128), vh[3], vl[3]);
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
-                            mma(T{}, o[h][j], vh, wh[h][f][0], wh[h][f][1]);
-                            mma(T{}, o[h][j], vh, wl[h][f][0], wl[h][f][1]);
-                            mma(T{}, o[h][j], vl, wh[h][f][0], wh[h][f][1]);
+                            mma(T{}, tile[h], vl, wh[h][f][0], wh[h][f][1]);
+                            mma(T{}, tile[h], vh, wl[h][f][0], wl[h][f][1]);
+                            mma(T{}, tile[h], vh, wh[h][f][0], wh[h][f][1]);
                         }
                     }
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[h][j][e] += tile[h][e];
+                }
             }
         }
         __syncwarp();
