@@ -1090,8 +1090,8 @@ auto with_shape(int32_t group, int32_t head_dim, F &&f) {
     using dcp::AttentionShape;
     if constexpr (T::kPerWord == 2) {
         if (head_dim <= 64)
-            return group <= 8    ? f(AttentionShape<T, 64, 1, 4, 6, 2>{})
-                   : group <= 16 ? f(AttentionShape<T, 64, 2, 4, 6, 2>{})
+            return group <= 8    ? f(AttentionShape<T, 64, 1, 4, 4, 3>{})
+                   : group <= 16 ? f(AttentionShape<T, 64, 2, 4, 4, 3>{})
                                  : f(AttentionShape<T, 64, 4, 4, 4, 2>{});
         if (head_dim <= 128)
             return group <= 8    ? f(AttentionShape<T, 128, 1, 4, 2, 3>{})
