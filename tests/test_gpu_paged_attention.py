@@ -5,6 +5,9 @@ outputs carry guard bands."""
 from __future__ import annotations
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -334,3 +337,86 @@ def test_own_workspace_and_refusals():
         dcp.paged_attention(q, k, v, table, seq, scale=math.nan)
     with pytest.raises(dcp.DCPError):
         dcp.paged_attention(q, k, v, table, seq, shard=2, num_shards=2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("page", [16, 5])
+def test_broadcast_cache_and_shared_tensor(dtype, page):
+    """One key head seen as four (stride 0) and values that are the keys."""
+    case = ref.PagedCase([50, 17], 1, 64, page, dtype, seed=31)
+    k, _, table = case.gpu()
+    q = query(2, 8, 64, dtype, 31)
+    seq = torch.tensor(case.lens, dtype=torch.int32, device="cuda")
+    out, lse = dcp.paged_attention(q.cuda(), k.expand(-1, -1, 4, -1), k.expand(-1, -1, 4, -1), table, seq)
+    keys = [x.expand(-1, 4, -1) for x in case.keys]
+    r = ref.attention(q, keys, keys, float(np.float32(0.125)))
+    ref.assert_attention(out, lse, r, 50, dtype)
+
+
+@pytest.mark.parametrize("page", [16, 24, 5])
+def test_a_page_named_twice_and_wide_tables(page):
+    """A table that names one page several times, with room for many more than are used."""
+    case = ref.PagedCase([2 * page, page], 2, 64, page, "bf16", seed=32)
+    k, v, table = case.gpu()
+    wide = torch.full((2, 4000), -1, dtype=torch.int32, device="cuda")
+    wide[0, :5] = table[0, 0]
+    wide[1, 0], wide[1, 1], wide[1, 2] = table[0, 1], table[1, 0], table[0, 1]
+    lens = [5 * page - 3, 2 * page + 1]
+    q = query(2, 6, 64, "bf16", 32)
+    out, lse = dcp.paged_attention(q.cuda(), k, v, wide, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    first, second = slice(0, page), slice(page, 2 * page)
+    keys, values = [], []
+    for src, dst in ((case.keys, keys), (case.values, values)):
+        dst.append(torch.cat([src[0][first]] * 5)[:lens[0]])
+        dst.append(torch.cat([src[0][second], src[1][first], src[0][second]])[:lens[1]])
+    r = ref.attention(q, keys, values, float(np.float32(0.125)))
+    ref.assert_attention(out, lse, r, max(lens), "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_forty_thousand_positions(dtype):
+    check(ref.PagedCase([40003], 1, 64, 32, dtype, seed=33), H=2, with_logits=False)
+
+
+def test_integer_scale_and_keyword_streams():
+    case = ref.PagedCase([30], 1, 64, 16, "bf16", seed=34)
+    k, v, table = case.gpu()
+    q = query(1, 2, 64, "bf16", 34, std=0.1).cuda()
+    seq = torch.tensor([30], dtype=torch.int32, device="cuda")
+    one, two = dcp.paged_attention(q, k, v, table, seq, scale=1), dcp.paged_attention(q, k, v, table, seq, scale=1.0)
+    assert torch.equal(one[0], two[0])
+    out, lse = torch.empty_like(q), torch.empty(1, 2, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    dcp.dcp_paged_attention(q, k, v, table, seq, out, lse, scale=1.0, stream=s)
+    s.synchronize()
+    assert torch.equal(out, two[0]) and torch.equal(lse, two[1])
+
+
+def test_capture_without_a_call_before():
+    """A graph captured by a process that has not launched any of these kernels."""
+    code = """
+import torch, decode_context_attention_dcp_b200 as dcp
+dcp.library()
+k = torch.randn(8, 16, 2, 64, device="cuda").bfloat16(); v = torch.randn_like(k)
+q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+t = torch.arange(8, dtype=torch.int32, device="cuda").reshape(2, 4)
+n = torch.tensor([50, 3], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out, lse = dcp.paged_attention(q, k, v, t, n)
+g.replay()
+torch.cuda.synchronize()
+want = dcp.paged_attention(q, k, v, t, n)
+assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+    assert res.returncode == 0 and "captured" in res.stdout, res.stderr[-2000:]
+
+
+def test_no_wait_ran_out():
+    """Last: every copy of the tests above arrived in time."""
+    assert dcp.dcp_wait_timeouts() == 0

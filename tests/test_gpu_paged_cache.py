@@ -114,6 +114,34 @@ def test_append_many_requests_and_strided_rows():
     assert same_bits(k, want)
 
 
+@pytest.mark.parametrize("heads", [33, 70])
+def test_append_many_heads_and_tokens(heads):
+    check_append([700, 3, 1400], [0, 700, 703, 1900], 1905, heads, 8, 16, "bf16", n=1)
+
+
+def test_append_on_another_stream_and_in_a_graph():
+    lens, T = [20, 33], 4
+    case = ref.PagedCase(lens, 2, 64, 16, "bf16", seed=9)
+    k, v, table = case.gpu()
+    new = torch.randn(T, 2, 64, device="cuda").to(torch.bfloat16)
+    want = append_ref(case.k, new.cpu(), case.table, lens, [0, 1, 4], 16, 0, 1, 1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    seq, starts = i32(lens), i32([0, 1, 4])
+    torch.cuda.synchronize()
+    dcp.dcp_kv_append(new, new, k, v, table, seq, starts, stream=s)
+    s.synchronize()
+    assert same_bits(k, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dcp.dcp_kv_append(new, new, k, v, table, seq, starts)
+    new.copy_(torch.randn_like(new))
+    seq.copy_(torch.tensor([19, 30], dtype=torch.int32))
+    graph.replay()
+    want = append_ref(want, new.cpu(), case.table, [19, 30], [0, 1, 4], 16, 0, 1, 1)
+    assert same_bits(k, want)
+
+
 # ---- accumulated weights --------------------------------------------------------------------------
 def check_weights(B, H, heads, cap, lens, base_e=True, lo_pad=0, w_pad=0, seq=None, offset=0, **kw):
     g = torch.Generator().manual_seed(B * 100 + H)
@@ -251,6 +279,47 @@ def test_evict_pages(layout, page, new_page):
 @pytest.mark.parametrize("keep", [1, 2, 1023, 1024, 5000])
 def test_evict_long(keep):
     check_evict([5000, 4999, 2600], 1, 64, 16, keep, keep // 4)
+
+
+@pytest.mark.parametrize("n", [4096, 4097, 20011, 49152, 49153])
+def test_evict_around_the_sizes_that_change_the_kernel(n):
+    check_evict([n, n - 1], 1, 8, 64, n // 3, 17, seed=n)
+
+
+def test_evict_long_rows_with_ties():
+    g = torch.Generator().manual_seed(3)
+    w = torch.randint(0, 3, (2, 1, 30000), generator=g).float()
+    check_evict([30000, 29999], 1, 8, 64, 12000, 100, weights=w)
+    w = torch.randint(0, 3, (1, 1, 60000), generator=g).float()
+    check_evict([60000], 1, 8, 64, 25000, 0, weights=w)
+
+
+def test_evict_on_another_stream_and_in_a_graph():
+    case = ref.PagedCase([100, 30], 2, 64, 16, "bf16", seed=12)
+    k, v, table = case.gpu()
+    w = torch.rand(2, 2, 100, device="cuda")
+    new = torch.arange(6, dtype=torch.int32, device="cuda").reshape(2, 3)
+    ko, vo = torch.zeros(6, 16, 2, 64, dtype=k.dtype, device="cuda"), torch.zeros(6, 16, 2, 64, dtype=k.dtype, device="cuda")
+    seq = i32([100, 30])
+    want = dcp.kv_evict(w, k, v, table, seq, new, 40, 4, k_out=ko, v_out=vo)
+    torch.cuda.synchronize()
+    first = ko.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = dcp.kv_evict(w, k, v, table, seq, new, 40, 4, k_out=ko, v_out=vo)
+    ko.zero_()
+    graph.replay()
+    assert torch.equal(ko, first) and all(torch.equal(a, b) for a, b in zip(got, want))
+    w.copy_(torch.rand(2, 2, 100, device="cuda"))
+    graph.replay()
+    for h in range(2):
+        assert got[0][0, h].tolist() == ref.select(w[0, h].cpu().numpy(), 40, 4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    kept, nl, nw = (torch.empty_like(x) for x in got)
+    dcp.dcp_kv_evict(w, k, v, table, seq, ko, vo, new, 40, 4, kept, nl, nw, stream=s)
+    s.synchronize()
+    assert torch.equal(kept, got[0]) and torch.equal(nw, got[2])
 
 
 def test_evict_very_long():
