@@ -322,7 +322,7 @@ int32_t check_common(const char *fn, int32_t dtype, int32_t N, int64_t B, int64_
 
 extern "C" {
 
-int32_t dcp_version(void) { return 10000; }
+int32_t dcp_version(void) { return 10100; }
 
 int32_t dcp_wait_timeouts(uint64_t *count, int32_t reset) {
     if (!count) return fail(DCP_ERR_INVALID_ARG, "dcp_wait_timeouts: count is null");

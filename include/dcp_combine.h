@@ -15,6 +15,9 @@
  *   dcp_combine_pack         a producer's split merge written straight into the send buffer
  *   dcp_unpack_combine       combine read straight out of the packed buffer
  *
+ * dcp_paged.h declares the second part: the paged key-value cache that the partial results come
+ * from.
+ *
  * Defining passages (web pages, by title and section):
  *   [COMBINE] vLLM API docs, vllm.v1.attention.ops.dcp_alltoall,
  *             _lse_weighted_combine: the combine rules.
@@ -270,7 +273,9 @@ int32_t dcp_unpack_combine(const void *recv_buf, void *result, float *global_lse
  * out the CTA is counted here and stops (after waiting, bounded, for the copies it has
  * issued), so the send buffer of that call is incomplete.  A tensor-copy CTA whose shared
  * memory cannot be placed on a 128-byte boundary is counted too and copies nothing (the
- * launch reserves the room to align it, so this does not happen).  A nonzero count therefore means a result is
+ * launch reserves the room to align it, so this does not happen).  The paged attention's waits for
+ * its tensor copies (dcp_paged.h) have the same limit and are counted here too, one per warp.  A
+ * nonzero count therefore means a result is
  * invalid (it never happens when the copies work).  Synchronises the device (the counter is
  * read from device memory); with reset != 0 the counter is cleared afterwards.  Returns
  * DCP_ERR_CUDA if the read fails.

@@ -100,6 +100,11 @@ int64_t dcp_paged_attention_workspace(int64_t H, int32_t heads, int32_t head_dim
  *
  * q           [B, H, head_dim] of kv->dtype; element (b, h, d) at b*q_stride_b + h*q_stride_h + d.
  * seq_lens    [B] int32, device.
+ * Pages of a multiple of 8 slots are read with tensor copies, through maps the call encodes (as
+ * dcp_pack does); a wait for them that runs out (never, while the copies work) is counted by
+ * dcp_wait_timeouts.  Other page sizes, and pools whose maps the driver refuses, are read row by row.
+ * Same result up to the order of sums.
+ *
  * result      [B, H, head_dim] of kv->dtype, contiguous.
  * lse         [B, H] fp32, contiguous.
  * logits      NULL, or fp32: x_p of head h goes to b*logits_stride_b + h*logits_stride_h + p for
