@@ -19,12 +19,17 @@
 // one fp32 partial (unnormalised row, maximum, sum) per share in the workspace, and
 // attention_join_kernel merges them in share order (no atomics: the same bits every time).
 //
+// Short calls (few requests, tables of a few tiles) instead give each request, key head and block of
+// heads a cluster of CTAs, which merge through distributed shared memory: one launch, no workspace.
+//
 // Inside a CTA each warp streams its own positions (warp w of NW takes every NW-th group of
 // 16) through its own ring of shared-memory stages, and keeps its own softmax state; warps meet
 // only where a request begins (the query) and ends (the merge).  A stage is filled by tensor
 // copies (a box of 8 or 16 slots of one page, 128 bytes of each row) where the page size is a
 // multiple of 8, else row by row with cp.async.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "dcp_paged.cuh"
 
@@ -277,7 +282,7 @@ struct PoolMaps {
     CUtensorMap k, v;
 };
 
-template <class S>
+template <class S, bool CLUSTER>
 __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     attention_stream_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ PoolMaps maps) {
     using T = typename S::T;
@@ -289,6 +294,9 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     __shared__ uint32_t s_held[ST][NW];            // bit r: position r of the warp's stage counts
     __shared__ uint2 s_row[NW][WP];                // cp.async: offsets of the K and V rows being copied
     __shared__ uint64_t s_full[NW][ST];            // tensor copies: a stage's bytes have arrived
+    __shared__ float2 s_part[S::kHeads];           // cluster: maximum and sum of this CTA's heads
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");
     constexpr bool TENSOR = S::BOX > 0;
@@ -297,10 +305,25 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
         mbar_fence_init();
     }
 
-    // the share: all lengths summed in one block scan, then the request where it begins
     int64_t begin, count;
     Shares shares(0, 1);
-    {
+    TileIter ld;
+    if constexpr (CLUSTER) {
+        // one request, key head and head block per cluster, its tiles in even parts
+        const int seg = blockIdx.x / cluster.num_blocks(), hb = seg % a.head_blocks;
+        ld.b = seg / a.head_blocks;
+        ld.kvh = hb / a.row_blocks;
+        ld.rb = hb - ld.kvh * a.row_blocks;
+        ld.n = local_length(a.sh, a.seq_lens[ld.b], a.kv.capacity);
+        ld.nt = tiles_of(ld.n, TILE);
+        ld.next_seq = 0;
+        shares = Shares(ld.nt, cluster.num_blocks());
+        begin = shares.begin(cluster.block_rank());
+        count = shares.begin(cluster.block_rank() + 1) - begin;
+        ld.t = (int)begin;
+        __syncwarp();  // the warp's barriers are initialised
+    } else {
+        // the share: all lengths summed in one block scan, then the request where it begins
         const int per = (a.B - 1) / S::kThreads + 1;
         const int b0 = (int)min((int64_t)tid * per, (int64_t)a.B), b1 = (int)min((int64_t)b0 + per, (int64_t)a.B);
         int64_t mine = 0;
@@ -342,19 +365,21 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
             s_where[2] = (int)(rest - (int64_t)hb * nt);
         }
         __syncthreads();
+        ld.b = s_where[0];
+        ld.kvh = s_where[1] / a.row_blocks;
+        ld.rb = s_where[1] - ld.kvh * a.row_blocks;
+        ld.t = s_where[2];
+        ld.next_seq = a.seq_lens[ld.b];
+        iter_request<TILE>(a, ld);
     }
-    TileIter ld;
-    ld.b = s_where[0];
-    ld.kvh = s_where[1] / a.row_blocks;
-    ld.rb = s_where[1] - ld.kvh * a.row_blocks;
-    ld.t = s_where[2];
-    ld.next_seq = a.seq_lens[ld.b];
-    iter_request<TILE>(a, ld);
     TileIter cp = ld;
+    const int ld0_b = ld.b, ld0_kvh = ld.kvh, ld0_rb = ld.rb;  // cluster: its request, key head and head block
 
     const uint32_t stages = smem_addr(smem) + warp * (ST * S::kStage);
     const uint32_t queries = smem_addr(smem) + NW * ST * S::kStage;
     uint2 *const query_pairs = reinterpret_cast<uint2 *>(smem + NW * ST * S::kStage);  // fp32
+    float *const cluster_rows = reinterpret_cast<float *>(smem + NW * ST * S::kStage);  // this CTA's rows at the merge
+    static_assert(!CLUSTER || S::kQueries >= S::kHeads * DP * 4, "the query's buffers hold the rows");
 
     // What this lane copies of a tile: cp.async, row lane mod 16; tensor copies, box `lane` of kBoxes (K's
     // then V's, row groups of BOX slots, panels).  Its page is read one tile ahead.
@@ -862,7 +887,10 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                         acc.z = fmaf(v.z, f, acc.z);
                         acc.w = fmaf(v.w, f, acc.w);
                     }
-                    if (whole) {
+                    if constexpr (CLUSTER) {  // the query's buffers are free now
+                        *reinterpret_cast<float4 *>(cluster_rows + (h0 * 8 + r) * DP + c * 4) = acc;
+                        if (c == 0) s_part[h0 * 8 + r] = make_float2(top, total);
+                    } else if (whole) {
                         write_result<T>(a, cp.b, cp.kvh * a.group + head0 + h0 * 8 + r, c * 4, acc, top, total);
                     } else {
                         const int64_t at = part * S::kHeads + h0 * 8 + r;
@@ -873,7 +901,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                 __syncthreads();
             }
             if (TENSOR) fence_proxy_async();  // the rows written above, before the stage's next tensor copy
-            if (i + 1 == count && tid == 0) {
+            if (!CLUSTER && i + 1 == count && tid == 0) {
                 int4 spill = make_int4(0, cp.b, cp.kvh, cp.rb);
                 // parts: this share and those up to the one with the request's last tile
                 if (first_t == 0 && !last)
@@ -883,6 +911,42 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
         }
         cp_stage = cp_stage + 1 == ST ? 0 : cp_stage + 1;
         iter_next<TILE>(a, cp);
+    }
+    if constexpr (CLUSTER) {
+        if (count == 0)
+            for (int r = tid; r < S::kHeads; r += S::kThreads) s_part[r] = make_float2(-INFINITY, 0.f);
+        cluster.sync();
+        constexpr int kMost = 8;
+        const int ctas = (int)cluster.num_blocks(), head0 = ld0_rb * S::kHeads;
+        const int rows = min(S::kHeads, a.group - head0);
+        for (int x = (int)cluster.block_rank() * S::kThreads + tid; x < rows * (DP / 4); x += ctas * S::kThreads) {
+            const int r = x / (DP / 4), c = x - r * (DP / 4);
+            float2 st[kMost];
+            float4 v[kMost];
+#pragma unroll
+            for (int k = 0; k < kMost; ++k) {
+                const int from = min(k, ctas - 1);
+                st[k] = *cluster.map_shared_rank(&s_part[r], from);
+                v[k] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(cluster_rows + r * DP + c * 4, from));
+            }
+            float top = -INFINITY, total = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMost; ++k) top = fmaxf(top, st[k].x);
+            const float base = finite_or_zero_max(top);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMost; ++k) {
+                if (k >= ctas || (st[k].x == -INFINITY && st[k].y == 0.f)) continue;  // its rows may hold anything
+                const float f = exp2_fast(st[k].x - base);
+                total = fmaf(st[k].y, f, total);
+                acc.x = fmaf(v[k].x, f, acc.x);
+                acc.y = fmaf(v[k].y, f, acc.y);
+                acc.z = fmaf(v[k].z, f, acc.z);
+                acc.w = fmaf(v[k].w, f, acc.w);
+            }
+            write_result<T>(a, ld0_b, ld0_kvh * a.group + head0 + r, c * 4, acc, top, total);
+        }
+        cluster.sync();  // no CTA leaves while another reads its shared memory
     }
     if (TENSOR && late) {  // copies may still be on their way into this CTA's shared memory: wait, bounded
         const uint64_t t0 = global_ns();
@@ -1036,19 +1100,54 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
 
 namespace dcp_host {
 
+// CTAs per request, key head and head block of a short call, 0 where the tiles are shared evenly
+// instead: as many as leave all of them resident, at most 8 and at most one per tile of the longest
+// request that the table can hold, if each then has at most kClusterTiles tiles.
+constexpr int64_t kClusterTiles = 4;
+
+inline int cluster_size(int64_t segments, int64_t tiles, int64_t most) {
+    int c = 1;
+    while (c < 8 && c < tiles && 2 * c * segments <= most) c *= 2;
+    return segments * c <= most && tiles <= kClusterTiles * c ? c : 0;
+}
+
 template <class S>
 int32_t launch_stream(dcp::AttentionArgs a, const dcp::PoolMaps &maps, cudaStream_t stream) {
     using T = typename S::T;
-    static InstanceCache cache;
     const char *fn = "dcp_paged_attention";
-    if (!reserve_smem(dcp::attention_stream_kernel<S>, cache, S::kSmem))
-        return fail(DCP_ERR_CUDA, "%s: cannot reserve shared memory", fn);
     a.row_blocks = (a.group + S::kHeads - 1) / S::kHeads;
     a.head_blocks = a.kv.heads * a.row_blocks;
     const int64_t most = (int64_t)sm_count() * S::CTAS;
+    if constexpr (S::NH <= 2) {
+        const int64_t segments = (int64_t)a.B * a.head_blocks;
+        const int ctas = cluster_size(segments, a.kv.capacity / S::TILE + 1, most);
+        if (ctas) {
+            static InstanceCache cache;
+            if (!reserve_smem(dcp::attention_stream_kernel<S, true>, cache, S::kSmem))
+                return fail(DCP_ERR_CUDA, "%s: cannot reserve shared memory", fn);
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3((unsigned)(segments * ctas));
+            cfg.blockDim = dim3(S::kThreads);
+            cfg.dynamicSmemBytes = S::kSmem;
+            cfg.stream = stream;
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)ctas;
+            attr.val.clusterDim.y = 1;
+            attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (cudaLaunchKernelEx(&cfg, dcp::attention_stream_kernel<S, true>, a, maps) != cudaSuccess)
+                return launch_status(fn);
+            return launch_status(fn);
+        }
+    }
+    static InstanceCache cache;
+    if (!reserve_smem(dcp::attention_stream_kernel<S, false>, cache, S::kSmem))
+        return fail(DCP_ERR_CUDA, "%s: cannot reserve shared memory", fn);
     const int64_t tiles = (int64_t)a.B * a.head_blocks * (a.kv.capacity / S::TILE + 1);
     const int grid = (int)(tiles < most ? tiles : most);
-    dcp::attention_stream_kernel<S><<<grid, S::kThreads, S::kSmem, stream>>>(a, maps);
+    dcp::attention_stream_kernel<S, false><<<grid, S::kThreads, S::kSmem, stream>>>(a, maps);
     int32_t st = launch_status(fn);
     if (st != DCP_OK) return st;
     // the join's launch overlaps the stream's end; its blocks wait for it before they read

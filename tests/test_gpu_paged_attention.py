@@ -69,29 +69,46 @@ def check(case: ref.PagedCase, H: int, std=1.0, base_e=True, scale=None, held=No
 RAGGED = [0, 1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 200]
 
 
+# A table of a few tiles gives each request a cluster of blocks; one that could hold more has the
+# tiles shared evenly over the device: the tests below run both on the same requests.
+WIDE = 700
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("D", [8, 16, 64, 80, 96, 128, 192, 256])
-def test_head_dims_and_lengths(dtype, D):
-    check(ref.PagedCase(RAGGED, 2, D, 16, dtype, seed=D), H=8)
+@pytest.mark.parametrize("width", [None, WIDE])
+def test_head_dims_and_lengths(dtype, D, width):
+    check(ref.PagedCase(RAGGED, 2, D, 16, dtype, seed=D, width=width), H=8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[1], [64], [65, 0], [300], [129, 500, 17], [1000, 2, 0, 600], [1500]])
+def test_few_requests(dtype, D, lens):
+    """Clusters of one to eight blocks, some of them without a tile."""
+    check(ref.PagedCase(lens, 2, D, 16, dtype, seed=len(lens) + D), H=6)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("H,heads", [(1, 1), (3, 3), (5, 1), (8, 8), (14, 2), (16, 1), (17, 1), (32, 1), (33, 1),
                                      (64, 2), (100, 2), (128, 1), (96, 8)])
-def test_head_groups(dtype, H, heads):
-    check(ref.PagedCase([0, 1, 37, 150, 64], heads, 64, 16, dtype, seed=H), H=H)
+@pytest.mark.parametrize("width", [None, WIDE])
+def test_head_groups(dtype, H, heads, width):
+    check(ref.PagedCase([0, 1, 37, 150, 64], heads, 64, 16, dtype, seed=H, width=width), H=H)
 
 
 @pytest.mark.parametrize("H,heads,D", [(48, 1, 128), (33, 1, 256), (40, 2, 192), (16, 1, 256), (20, 1, 256)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
-def test_wide_groups_of_wide_heads(dtype, H, heads, D):
-    check(ref.PagedCase([70, 0, 129], heads, D, 32, dtype, seed=H + D), H=H)
+@pytest.mark.parametrize("width", [None, WIDE])
+def test_wide_groups_of_wide_heads(dtype, H, heads, D, width):
+    check(ref.PagedCase([70, 0, 129], heads, D, 32, dtype, seed=H + D, width=width), H=H)
 
 
 @pytest.mark.parametrize("page", [1, 2, 5, 8, 13, 16, 24, 32, 48, 64, 100, 128, 256])
 @pytest.mark.parametrize("layout", ["slots", "heads", "mixed"])
-def test_pages_and_layouts(page, layout):
-    check(ref.PagedCase(RAGGED, 2, 128, page, "bf16", layout, seed=page), H=8)
+@pytest.mark.parametrize("width", [None, 12000])
+def test_pages_and_layouts(page, layout, width):
+    check(ref.PagedCase(RAGGED, 2, 128, page, "bf16", layout, seed=page, width=width), H=8)
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "fp32"])
@@ -257,8 +274,9 @@ def test_special_values():
     assert torch.isnan(lse[3]).all() and not torch.isfinite(lse[2]).any()
 
 
-def test_same_bits_every_time():
-    case = ref.PagedCase([3000, 17, 900], 2, 128, 16, "bf16", seed=15)
+@pytest.mark.parametrize("lens", [[3000, 17, 900], [200, 17, 90]])
+def test_same_bits_every_time(lens):
+    case = ref.PagedCase(lens, 2, 128, 16, "bf16", seed=15)
     k, v, table = case.gpu()
     q = query(3, 8, 128, "bf16", 15).cuda()
     seq = torch.tensor(case.lens, dtype=torch.int32, device="cuda")
@@ -289,9 +307,10 @@ def test_other_stream_and_two_at_once():
         assert torch.equal(o, want[0]) and torch.equal(l, want[1])
 
 
-def test_graph_replay_with_other_lengths():
+@pytest.mark.parametrize("width", [None, WIDE])
+def test_graph_replay_with_other_lengths(width):
     """Captured once (two calls in one graph), replayed with other lengths and queries."""
-    case = ref.PagedCase([900, 64, 200], 2, 64, 16, "bf16", seed=17)
+    case = ref.PagedCase([900, 64, 200], 2, 64, 16, "bf16", seed=17, width=width)
     k, v, table = case.gpu()
     q = query(3, 8, 64, "bf16", 17).cuda()
     seq = torch.tensor(case.lens, dtype=torch.int32, device="cuda")
