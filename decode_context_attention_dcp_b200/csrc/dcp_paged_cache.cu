@@ -253,6 +253,23 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t mine, uint32_t *sums, 
     return __shfl_sync(0xffffffffu, all - own, warp) + upto - mine;
 }
 
+constexpr int kMoveRows = 64;  // kept rows a block moves at a time
+
+// The places of kept position p (-1: none) of request b and key head h, the i-th one kept.
+__device__ __forceinline__ RowMove place(const EvictArgs &a, int b, int h, int32_t p, int i) {
+    RowMove mv{-1, 0, 0, 0};
+    int64_t sp, dp;
+    uint32_t ss, ds;
+    if (p >= 0 && locate(a.src, a.src.table + b * a.src.table_stride, (uint32_t)p, sp, ss) &&
+        locate(a.dst, a.dst.table + b * a.dst.table_stride, (uint32_t)i, dp, ds)) {
+        mv.k_from = sp * a.src.k_page_w + ss * a.src.k_slot_w + h * a.src.k_head_w;
+        mv.v_from = sp * a.src.v_page_w + ss * a.src.v_slot_w + h * a.src.v_head_w;
+        mv.k_to = dp * a.dst.k_page_w + ds * a.dst.k_slot_w + h * a.dst.k_head_w;
+        mv.v_to = dp * a.dst.v_page_w + ds * a.dst.v_slot_w + h * a.dst.v_head_w;
+    }
+    return mv;
+}
+
 // How a selection kernel holds a row's weights (as keys):
 //   kRegisters  one CTA, kKeys adjacent weights per thread in registers;
 //   kShared     one CTA, in shared memory: longer rows without a second reading;
@@ -268,8 +285,13 @@ enum KeyStore { kRegisters, kShared, kCluster };
 //   output: keys above it and the first ties are placed by a prefix sum in position order.
 // Positions past the end enter as key 0: below or equal to every weight and after it, they are
 // never among the kept.
-template <int THREADS, int STORE>
-__global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constant__ EvictArgs a) {
+//
+// MOVE (short rows): `parts` CTAs per row, each of which selects all of the row for itself and then
+// writes and moves its own kMoveRows of the kept ones: one launch, no CTA waits for another.
+template <int THREADS, int STORE, bool MOVE>
+__global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constant__ EvictArgs a, FastDiv row_chunks,
+                                                            int parts) {
+    static_assert(!MOVE || (STORE == kRegisters && THREADS == kCopyThreads), "MOVE: short rows, copy_rows' block");
     constexpr bool CLUSTER = STORE == kCluster, SHARED = STORE == kShared;
     constexpr int W = THREADS / 32, BPT = kBins / THREADS;  // bins per thread
     static_assert(BPT % 2 == 0 && (SHARED || THREADS * kKeys < 65536), "pairs of bins; 16-bit counts");
@@ -279,16 +301,19 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
     __shared__ uint32_t s_total[1];
     __shared__ uint32_t s_digit, s_need;
     cg::cluster_group cluster = cg::this_cluster();
+    __shared__ RowMove moves[MOVE ? kMoveRows : 1];
+    __shared__ int32_t s_kept[MOVE ? kMoveRows : 1];
     const int ctas = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
     const int tid = threadIdx.x;
-    const int row = blockIdx.x / ctas, b = row / a.src.heads, j = row - b * a.src.heads;
+    const int sharing = MOVE ? parts : ctas;  // CTAs of this row, and this one's number among them
+    const int part = blockIdx.x % sharing, row = blockIdx.x / sharing, b = row / a.src.heads, j = row - b * a.src.heads;
     const float *w = a.weights + b * a.w_sb + j * a.w_sh;
     float *nw = a.new_weights + b * a.nw_sb + j * a.nw_sh;
     int32_t *kept = a.kept + (int64_t)row * a.keep;
     const int cap = a.src.capacity < a.cap ? a.src.capacity : a.cap;
     const int n = local_length(a.sh, a.seq_lens[b], cap);
     const int m = n < a.keep ? n : a.keep;
-    if (j == 0 && rank == 0 && tid == 0) a.new_lens[b] = m;
+    if (j == 0 && part == 0 && tid == 0) a.new_lens[b] = m;
     const bool full = n <= a.keep;
     const uint32_t body = full ? 0 : (uint32_t)(n - a.recent);  // positions that compete
     const uint32_t want = full ? 0 : (uint32_t)(a.keep - a.recent);
@@ -347,14 +372,27 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
             load(mine, first);
         }
     }
-    // the outputs that do not depend on the selection: the last positions, and what is left over
-    const int step = ctas * THREADS, id = rank * THREADS + tid;
-    for (int64_t p = (int64_t)body + id; p < n; p += step) {
-        const int64_t to = (int64_t)want + (p - body);
+    // kept position p becomes entry `to`, which is one of this CTA's own
+    const uint32_t own0 = MOVE ? (uint32_t)part * kMoveRows : 0;
+    auto keep = [&](uint32_t to, uint32_t p, float weight) {
         kept[to] = (int32_t)p;
-        nw[to] = w[p];
+        nw[to] = weight;
+        if (MOVE) s_kept[to - own0] = (int32_t)p;
+    };
+    auto owned = [&](uint32_t to) { return MOVE ? to - own0 < (uint32_t)kMoveRows : true; };
+    // the outputs that do not depend on the selection: the last positions, and what is left over
+    const int step = sharing * THREADS, id = part * THREADS + tid;
+    if constexpr (MOVE) {
+        const int64_t i = (int64_t)own0 + tid;
+        if (tid < kMoveRows) {
+            s_kept[tid] = -1;
+            if (i >= want && i < m) keep((uint32_t)i, (uint32_t)(body + i - want), w[body + i - want]);
+            if (i >= m && i < a.keep) kept[i] = -1;
+        }
+    } else {
+        for (int64_t p = (int64_t)body + id; p < n; p += step) keep((uint32_t)(want + (p - body)), (uint32_t)p, w[p]);
+        for (int64_t i = (int64_t)m + id; i < a.keep; i += step) kept[i] = -1;
     }
-    for (int64_t i = (int64_t)m + id; i < a.keep; i += step) kept[i] = -1;
     {
         // to the next 16 bytes one by one, then 4 at a time
         const int64_t lead = m + ((4 - ((reinterpret_cast<uintptr_t>(nw + m) >> 2) & 3)) & 3);
@@ -364,12 +402,14 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
             *reinterpret_cast<float4 *>(nw + i) = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int64_t i = end4 + id; i < a.new_cap; i += step) nw[i] = 0.f;
     }
-    if (!want) return;  // the same for the whole cluster
+    if (!MOVE && !want) return;  // the same for the whole cluster
     __syncthreads();
 
     uint32_t prefix = 0, need = want;
+    // MOVE: without a selection (want == 0) these passes see no key and are not used
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
+        if (MOVE && !want) break;
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         auto count = [&](uint32_t key) {
             if (pass == 0 || (key >> (shift + bits)) == prefix >> (shift + bits))
@@ -456,15 +496,14 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
             // to < want always, unless the weights changed meanwhile
             if ((key > prefix || (key == prefix && my_ties < need)) && to < want) {
                 const uint32_t p = 32 * i + lane;
-                kept[to] = (int32_t)p;
-                nw[to] = key_weight(key, w + p);
+                keep(to, p, key_weight(key, w + p));
             }
             above += __popc(some_gt);
             ties += __popc(some_eq);
         }
     } else {
         uint32_t above0 = 0, ties0 = 0;  // in earlier rounds
-        for (uint32_t q = 0; q < body; q += round) {
+        for (uint32_t q = 0; q < (want ? body : 0); q += round) {
             const uint32_t p = q + mine;
             uint32_t gt = 0, eq = 0;  // bit i: key i
             {
@@ -502,20 +541,21 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
                 const bool is_eq = (eq >> i) & 1u;
                 if (!is_eq || ties < need) {
                     const uint32_t to = above + (ties < need ? ties : need);
-                    if (to < want) {  // always, unless the weights changed meanwhile
-                        kept[to] = (int32_t)(p + i);
-                        nw[to] = __ldg(w + p + i);
-                    }
+                    if (to < want && owned(to)) keep(to, p + i, __ldg(w + p + i));  // < want: unless the weights changed
                 }
                 if (is_eq) ++ties; else ++above;
             }
         }
     }
+    if constexpr (MOVE) {
+        __syncthreads();
+        if (tid < kMoveRows) moves[tid] = place(a, b, j, s_kept[tid], (int)own0 + tid);
+        __syncthreads();
+        copy_rows<4>(moves, kMoveRows, row_chunks, a.src.k, a.src.v, a.dst.k, a.dst.v);
+    }
 }
 
-constexpr int kMoveRows = 64;  // kept rows a block moves at a time
-
-// Kept rows to their new places: one thread per row finds them, all threads copy.
+// Kept rows to their new places.
 __global__ void __launch_bounds__(kCopyThreads) kv_move_kernel(const __grid_constant__ EvictArgs a, FastDiv chunks,
                                                                int64_t rows, int pieces) {
     __shared__ RowMove moves[kMoveRows];
@@ -525,21 +565,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_move_kernel(const __grid_cons
         const int i0 = (int)(g - row * pieces) * kMoveRows;
         const int b = (int)(row / a.src.heads), h = (int)(row - (int64_t)b * a.src.heads);
         const int rn = min(kMoveRows, a.keep - i0);
-        if (threadIdx.x < rn) {
-            const int i = i0 + threadIdx.x;
-            const int32_t p = a.kept[row * a.keep + i];
-            RowMove mv{-1, 0, 0, 0};
-            int64_t sp, dp;
-            uint32_t ss, ds;
-            if (p >= 0 && locate(a.src, a.src.table + b * a.src.table_stride, (uint32_t)p, sp, ss) &&
-                locate(a.dst, a.dst.table + b * a.dst.table_stride, (uint32_t)i, dp, ds)) {
-                mv.k_from = sp * a.src.k_page_w + ss * a.src.k_slot_w + h * a.src.k_head_w;
-                mv.v_from = sp * a.src.v_page_w + ss * a.src.v_slot_w + h * a.src.v_head_w;
-                mv.k_to = dp * a.dst.k_page_w + ds * a.dst.k_slot_w + h * a.dst.k_head_w;
-                mv.v_to = dp * a.dst.v_page_w + ds * a.dst.v_slot_w + h * a.dst.v_head_w;
-            }
-            moves[threadIdx.x] = mv;
-        }
+        if (threadIdx.x < rn) moves[threadIdx.x] = place(a, b, h, a.kept[row * a.keep + i0 + threadIdx.x], i0 + threadIdx.x);
         __syncthreads();
         copy_rows<4>(moves, rn, chunks, a.src.k, a.src.v, a.dst.k, a.dst.v);
         __syncthreads();
@@ -595,7 +621,7 @@ int32_t kv_weights(const dcp::WeightsArgs &a, cudaStream_t stream) {
     return launch_status("dcp_kv_weights");
 }
 
-template <int THREADS, int STORE>
+template <int THREADS, int STORE, bool MOVE = false>
 cudaError_t launch_select(const dcp::EvictArgs &a, int ctas, size_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.src.heads * ctas));
@@ -609,7 +635,7 @@ cudaError_t launch_select(const dcp::EvictArgs &a, int ctas, size_t smem, cudaSt
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = STORE == dcp::kCluster ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, dcp::kv_select_kernel<THREADS, STORE>, a);
+    return cudaLaunchKernelEx(&cfg, dcp::kv_select_kernel<THREADS, STORE, MOVE>, a, divisor(a.src.data_w / 4), ctas);
 }
 
 constexpr int64_t kMaxShared = 49152;  // weights a CTA's shared memory holds (192 KB)
@@ -617,12 +643,20 @@ constexpr int64_t kMaxShared = 49152;  // weights a CTA's shared memory holds (1
 int32_t kv_evict(const dcp::EvictArgs &a, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.B * a.src.heads;
     const int64_t longest = a.cap < a.src.capacity ? a.cap : a.src.capacity;  // the longest row there can be
+    const int64_t parts = (a.keep - 1) / dcp::kMoveRows + 1;
     cudaError_t e;
+    if (longest <= 256 * dcp::kKeys && rows * parts <= 3 * sm_count()) {
+        // all of it at once on the device: every CTA selects for itself (24 rows of up to 2000, 512 kept: 8.8 us,
+        // selection and moves apart 10.6; 512 CTAs for 128 rows of 4000: 16.1 against 15.0)
+        if (launch_select<256, dcp::kRegisters, true>(a, (int)parts, 0, stream) != cudaSuccess)
+            return launch_status("dcp_kv_evict");
+        return launch_status("dcp_kv_evict");
+    }
     if (longest <= 256 * dcp::kKeys) {
         e = launch_select<256, dcp::kRegisters>(a, 1, 0, stream);
     } else if (longest <= kMaxShared) {
         static InstanceCache cache;
-        if (!reserve_smem(dcp::kv_select_kernel<1024, dcp::kShared>, cache, kMaxShared * 4))
+        if (!reserve_smem(dcp::kv_select_kernel<1024, dcp::kShared, false>, cache, kMaxShared * 4))
             return fail(DCP_ERR_CUDA, "dcp_kv_evict: cannot reserve shared memory");
         e = launch_select<1024, dcp::kShared>(a, 1, (size_t)((longest + 31) / 32 * 128), stream);
     } else {
