@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
     // registers: this thread's keys start at `mine`, and every `round` after it
     const uint32_t round = (uint32_t)ctas * THREADS * kKeys;  // below 2^17
     const uint32_t mine = ((uint32_t)rank * THREADS + tid) * kKeys;
-    const uint32_t chunks = (body + 31) / 32 * 8;  // shared memory: whole warps of keys
+    const uint32_t chunks = (body + 127) / 128 * 32;  // shared memory: whole warps of chunks
 
     auto load = [&](uint32_t p, uint32_t *key) {
         if (p + kKeys <= body && (reinterpret_cast<uintptr_t>(w + p) & 15) == 0) {
@@ -476,36 +476,53 @@ __global__ void __launch_bounds__(THREADS) kv_select_kernel(const __grid_constan
     }
     // keys above `prefix` are kept, and the first `need` that equal it
     if constexpr (SHARED) {
-        // each warp owns a stretch of positions, 32 adjacent ones per step: a count, the warps' prefix sums,
-        // then the places by ballots
+        // each warp owns a stretch of positions, 128 adjacent ones per step (four per lane): a count, the
+        // warps' prefix sums, then the places by ballots
         const int lane = tid & 31, warp = tid >> 5;
-        const uint32_t *keys = reinterpret_cast<const uint32_t *>(s_keys);
-        const uint32_t words = chunks / 8, own = (words + W - 1) / W;
-        const uint32_t begin = min(warp * own, words), end = min(begin + own, words);
+        const uint32_t units = chunks / 32, own = (units + W - 1) / W;
+        const uint32_t begin = min(warp * own, units), end = min(begin + own, units);
         uint32_t gt = 0, eq = 0, total;
         for (uint32_t i = begin; i < end; ++i) {
-            const uint32_t key = keys[32 * i + lane];
-            gt += key > prefix;
-            eq += key == prefix;
+            const uint4 k = s_keys[32 * i + lane];
+            gt += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+            eq += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
         }
         // below 65536 keys: 16-bit halves do not overflow
         const uint32_t at = block_prefix<W>(gt | eq << 16, sums[3], total);
         const uint32_t start = __shfl_sync(0xffffffffu, at, 0);
-        uint32_t above = start & 0xffffu, ties = start >> 16;
+        uint32_t above = start & 0xffffu, ties = start >> 16;  // before the step
         const uint32_t lower = (1u << lane) - 1u;
         for (uint32_t i = begin; i < end; ++i) {
-            const uint32_t key = keys[32 * i + lane];
-            const unsigned some_gt = __ballot_sync(0xffffffffu, key > prefix);
-            const unsigned some_eq = __ballot_sync(0xffffffffu, key == prefix);
-            const uint32_t my_ties = ties + __popc(some_eq & lower);
-            const uint32_t to = above + __popc(some_gt & lower) + (my_ties < need ? my_ties : need);
-            // to < want always, unless the weights changed meanwhile
-            if ((key > prefix || (key == prefix && my_ties < need)) && to < want) {
-                const uint32_t p = 32 * i + lane;
-                keep(to, p, key_weight(key, w + p));
+            const uint4 k4 = s_keys[32 * i + lane];
+            const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+            uint32_t my_above = above, my_ties = ties;
+            unsigned any = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const unsigned some = __ballot_sync(0xffffffffu, key[e] > prefix);
+                my_above += __popc(some & lower);
+                above += __popc(some);
+                any |= key[e] == prefix;
             }
-            above += __popc(some_gt);
-            ties += __popc(some_eq);
+            if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const unsigned some = __ballot_sync(0xffffffffu, key[e] == prefix);
+                    my_ties += __popc(some & lower);
+                    ties += __popc(some);
+                }
+            }
+            const uint32_t p = 4 * (32 * i + lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool is_gt = key[e] > prefix, is_eq = key[e] == prefix;
+                if (is_gt || (is_eq && my_ties < need)) {
+                    const uint32_t to = my_above + (my_ties < need ? my_ties : need);
+                    if (to < want) keep(to, p + e, key_weight(key[e], w + p + e));  // < want: unless the weights changed
+                }
+                my_above += is_gt;
+                my_ties += is_eq;
+            }
         }
     } else {
         uint32_t above0 = 0, ties0 = 0;  // in earlier rounds
@@ -664,7 +681,7 @@ int32_t kv_evict(const dcp::EvictArgs &a, cudaStream_t stream) {
         static InstanceCache cache;
         if (!reserve_smem(dcp::kv_select_kernel<1024, dcp::kShared, false>, cache, kMaxShared * 4))
             return fail(DCP_ERR_CUDA, "dcp_kv_evict: cannot reserve shared memory");
-        e = launch_select<1024, dcp::kShared>(a, 1, (size_t)((longest + 31) / 32 * 128), stream);
+        e = launch_select<1024, dcp::kShared>(a, 1, (size_t)((longest + 127) / 128 * 512), stream);
     } else {
         // as many CTAs (at most 8) as hold the row in registers, as far as the grid's size allows
         int ctas = rows * 8 < (int64_t(1) << 31) ? 8 : 1;
