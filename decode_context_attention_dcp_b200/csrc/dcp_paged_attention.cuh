@@ -165,10 +165,10 @@ struct WeightShift<Fp16> {
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // ---- workspace --------------------------------------------------------------------------------
-// Two partials per CTA (the request it entered in the middle, the one it left unfinished): kRows
-// rows of DP floats each, then (maximum, sum) per row, then one int4 per CTA: the number of
+// Two partials per CTA (the request it entered in the middle, the one it left unfinished): ROWS query
+// heads' rows of DP floats each, then (maximum, sum) per row, then one int4 per CTA: the number of
 // parts of the request that starts in this CTA and is finished by later ones (0: none), its
-// request, key head and row block.
+// request, key head and head block.
 struct Workspace {
     float *rows;
     float2 *stats;
@@ -210,7 +210,7 @@ struct Shares {
     }
 };
 
-// Position in the sequence of tiles: tile t of nt of request b, key head kvh and row block rb; n
+// Position in the sequence of tiles: tile t of nt of request b, key head kvh and head block rb; n
 // is the request's local length.  The next request's length is read one request ahead.
 struct TileIter {
     int b, kvh, rb, t, n, nt, next_seq;

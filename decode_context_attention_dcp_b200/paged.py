@@ -201,6 +201,8 @@ def _attend(q, k_cache, v_cache, block_table, seq_lens, out, lse, world_size, sc
         scale = 1.0 / math.sqrt(D) if D else 1.0
     if workspace is None:
         workspace = _scratch(q, paged_attention_workspace(q, k_cache), stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     tail = (qb, qh, lb, lh, cap, scale, shard, num_shards, interleave, 1 if is_lse_base_on_e else 0, ws, wsb,
             _raw_stream(dev, stream))

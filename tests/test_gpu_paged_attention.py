@@ -344,6 +344,8 @@ def test_own_workspace_and_refusals():
     if n > 16:
         with pytest.raises(dcp.DCPError, match="workspace"):
             dcp.dcp_paged_attention(q, k, v, table, seq, out, lse, workspace=ws[:n - 16])
+    with pytest.raises(ValueError, match="workspace"):
+        dcp.dcp_paged_attention(q, k, v, table, seq, out, lse, workspace=ws[:1].expand(n))
     bad = [dict(q=q.float()), dict(q=q[..., ::2]), dict(table=table.long()), dict(table=table[:, :0].expand(2, 0)),
            dict(seq=seq.long()), dict(seq=seq.repeat(2)), dict(k=k[..., :32]), dict(v=v.half())]
     for kw in bad:
