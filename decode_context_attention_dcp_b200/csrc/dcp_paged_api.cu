@@ -44,8 +44,14 @@ int64_t attention_workspace(int32_t group, int32_t head_dim, int32_t dtype) {
     }
 }
 
+// Rows of `width` elements, n0 times n1 of them, of which neighbours share elements.
+bool rows_overlap(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width) {
+    return (n0 > 1 && s0 < width) || (n1 > 1 && s1 < width);
+}
+
 // `used`: the call reads the block table (it has requests), so its pointers must be there.
-int32_t check_cache(const char *fn, const dcp_paged_kv *kv, bool used, dcp::PagedCache &c) {
+// `written`: the call writes the pools, whose rows must then be apart.
+int32_t check_cache(const char *fn, const dcp_paged_kv *kv, bool used, bool written, dcp::PagedCache &c) {
     if (!kv) return fail(DCP_ERR_INVALID_ARG, "%s: the cache description is null", fn);
     const int es = elem_size(kv->dtype);
     if (es == 0) return fail(DCP_ERR_UNSUPPORTED_DTYPE, "%s: unsupported dtype %d", fn, (int)kv->dtype);
@@ -71,6 +77,10 @@ int32_t check_cache(const char *fn, const dcp_paged_kv *kv, bool used, dcp::Page
     if (!aligned(kv->block_table, 4)) return fail(DCP_ERR_MISALIGNED, "%s: block_table must be 4-byte aligned", fn);
     if (used && kv->max_pages > 0 && !kv->block_table) return fail(DCP_ERR_INVALID_ARG, "%s: null block_table", fn);
     if (used && kv->num_pages > 0 && (!kv->k || !kv->v)) return fail(DCP_ERR_INVALID_ARG, "%s: null cache pointer", fn);
+    for (int i = 0; written && i < 6; i += 3)
+        if (rows_overlap(kv->num_pages, st[i], kv->page_size, st[i + 1], kv->head_dim) ||
+            rows_overlap(kv->heads, st[i + 2], 1, 0, kv->head_dim))
+            return fail(DCP_ERR_INVALID_ARG, "%s: rows of the cache that is written overlap", fn);
     c.k = static_cast<uint32_t *>(kv->k);
     c.v = static_cast<uint32_t *>(kv->v);
     c.table = kv->block_table;
@@ -135,7 +145,7 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
                   float scale, int32_t shard, int32_t num_shards, int32_t interleave, int32_t is_lse_base_on_e,
                   void *workspace, int64_t workspace_bytes, void *cuda_stream) {
     dcp::AttentionArgs a{};
-    int32_t st = check_cache(fn, kv, B != 0, a.kv);
+    int32_t st = check_cache(fn, kv, B != 0, false, a.kv);
     if (st == DCP_OK) st = check_shards(fn, shard, num_shards, interleave, a.sh);
     if (st != DCP_OK) return st;
     const int es = elem_size(kv->dtype);
@@ -171,6 +181,8 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
         return fail(DCP_ERR_MISALIGNED, "%s: the query and the result must be 16-byte aligned", fn);
     if (!aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(logits, 4))
         return fail(DCP_ERR_MISALIGNED, "%s: seq_lens, lse and logits must be 4-byte aligned", fn);
+    if (logits && rows_overlap(B, logits_stride_b, H, logits_stride_h, logits_cap))
+        return fail(DCP_ERR_INVALID_ARG, "%s: the rows of logits overlap", fn);
     const int64_t need = attention_workspace((int32_t)(H / kv->heads), kv->head_dim, kv->dtype);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
@@ -245,7 +257,7 @@ int32_t dcp_kv_append(const dcp_paged_kv *kv, const void *k_new, const void *v_n
                       int32_t interleave, void *cuda_stream) {
     const char *fn = "dcp_kv_append";
     dcp::AppendArgs a{};
-    int32_t st = check_cache(fn, kv, T != 0 && num_reqs != 0, a.kv);
+    int32_t st = check_cache(fn, kv, T != 0 && num_reqs != 0, true, a.kv);
     if (st == DCP_OK) st = check_shards(fn, shard, num_shards, interleave, a.sh);
     if (st != DCP_OK) return st;
     const int es = elem_size(kv->dtype);
@@ -300,6 +312,8 @@ int32_t dcp_kv_weights(const float *logits, const float *global_lse, const int32
     if (!logits || !global_lse || !seq_lens || !weights) return fail(DCP_ERR_INVALID_ARG, "%s: null buffer pointer", fn);
     if (!aligned(logits, 4) || !aligned(global_lse, 4) || !aligned(seq_lens, 4) || !aligned(weights, 4))
         return fail(DCP_ERR_MISALIGNED, "%s: all arrays must be 4-byte aligned", fn);
+    if (rows_overlap(B, weights_stride_b, heads, weights_stride_h, cap))
+        return fail(DCP_ERR_INVALID_ARG, "%s: the rows of weights overlap", fn);
     a.logits = logits;
     a.lse = global_lse;
     a.seq_lens = seq_lens;
@@ -325,8 +339,8 @@ int32_t dcp_kv_evict(const dcp_paged_kv *src, const dcp_paged_kv *dst, const int
                      int32_t interleave, void *cuda_stream) {
     const char *fn = "dcp_kv_evict";
     dcp::EvictArgs a{};
-    int32_t st = check_cache(fn, src, B != 0, a.src);
-    if (st == DCP_OK) st = check_cache(fn, dst, B != 0, a.dst);
+    int32_t st = check_cache(fn, src, B != 0, false, a.src);
+    if (st == DCP_OK) st = check_cache(fn, dst, B != 0, true, a.dst);
     if (st == DCP_OK) st = check_shards(fn, shard, num_shards, interleave, a.sh);
     if (st != DCP_OK) return st;
     if (src->heads != dst->heads || src->head_dim != dst->head_dim || src->dtype != dst->dtype)
@@ -348,6 +362,8 @@ int32_t dcp_kv_evict(const dcp_paged_kv *src, const dcp_paged_kv *dst, const int
     if (!aligned(seq_lens, 4) || !aligned(weights, 4) || !aligned(new_weights, 4) || !aligned(kept, 4) ||
         !aligned(new_lens, 4))
         return fail(DCP_ERR_MISALIGNED, "%s: all arrays must be 4-byte aligned", fn);
+    if (rows_overlap(B, new_weights_stride_b, dst->heads, new_weights_stride_h, new_cap))
+        return fail(DCP_ERR_INVALID_ARG, "%s: the rows of new_weights overlap", fn);
     a.seq_lens = seq_lens;
     a.weights = weights;
     a.new_weights = new_weights;

@@ -93,6 +93,13 @@ def _done(status) -> bool:
     return status is not None
 
 
+def _check_ints(**values) -> None:
+    """Arguments that the C ABI takes as 32-bit integers (ctypes would cut them)."""
+    for what, n in values.items():
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{what}={n} is outside the range of 32-bit integers")
+
+
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, requests: int,
            what: str = "") -> _PagedKV:
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
@@ -108,6 +115,7 @@ def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tens
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != requests:
         raise ValueError(f"{what}block_table must be int32 [{requests}, max_pages], got {block_table.dtype} "
                          f"{tuple(block_table.shape)}")
+    _check_ints(page_size=page_size, heads=heads, D=D)
     width, (tb, te) = block_table.shape[1], block_table.stride()
     if width > 1 and te != 1:
         raise ValueError(f"{what}block_table must be contiguous in its last dimension")
@@ -184,6 +192,7 @@ def _scratch(like: torch.Tensor, nbytes: int, stream) -> torch.Tensor | None:
 def _attend(q, k_cache, v_cache, block_table, seq_lens, out, lse, world_size, scale, shard, num_shards, interleave,
             logits, is_lse_base_on_e, workspace, stream) -> None:
     dev = _cuda(q, k_cache, v_cache, block_table, seq_lens, out, lse, logits, workspace)
+    _check_ints(shard=shard, num_shards=num_shards, interleave=interleave)
     B, H, D = q.shape
     kv = _cache(k_cache, v_cache, block_table, B)
     _lens(seq_lens, B)
@@ -273,6 +282,7 @@ def dcp_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tenso
                                                   query_start_loc, shard, num_shards, interleave)):
         return
     dev = _cuda(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc)
+    _check_ints(shard=shard, num_shards=num_shards, interleave=interleave)
     R = seq_lens.numel()
     _lens(seq_lens, R)
     kv = _cache(k_cache, v_cache, block_table, R)
@@ -303,6 +313,7 @@ def dcp_kv_weights(logits: torch.Tensor, global_lse: torch.Tensor, seq_lens: tor
                                                  is_lse_base_on_e)):
         return
     dev = _cuda(logits, global_lse, seq_lens, weights)
+    _check_ints(shard=shard, num_shards=num_shards, interleave=interleave)
     if weights.dim() != 3 or logits.dim() != 3:
         raise ValueError("logits must be [B, H, cap] and weights [B, heads, cap]")
     B, H = logits.shape[:2]
@@ -327,6 +338,7 @@ def dcp_kv_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     new_cap >= keep] (the kept weights, then 0)."""
     dev = _cuda(weights, k_cache, v_cache, block_table, seq_lens, k_out, v_out, new_block_table, kept, new_lens,
                 new_weights)
+    _check_ints(shard=shard, num_shards=num_shards, interleave=interleave)
     B = seq_lens.numel()
     _lens(seq_lens, B)
     src = _cache(k_cache, v_cache, block_table, B)

@@ -384,6 +384,40 @@ def test_evict_helper_and_refusals():
         dcp.kv_evict(w[:1], k, v, table, i32([50, 10]), new, 20)
 
 
+def test_refused_arguments_of_all_calls():
+    """Integers that do not fit 32 bits are not cut, and outputs whose rows overlap are refused."""
+    case = ref.PagedCase([50, 10], 2, 64, 16, "bf16", seed=3)
+    k, v, table = case.gpu()
+    seq, starts = i32([50, 10]), i32([0, 1, 2])
+    q, new = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda"), k[0, :2].clone()
+    logits, lse = torch.zeros(2, 4, 64, device="cuda"), torch.zeros(2, 4, device="cuda")
+    w = torch.zeros(2, 2, 64, device="cuda")
+    out = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    new_table = torch.arange(4, dtype=torch.int32, device="cuda").reshape(2, 2)
+
+    def calls(**kw):
+        yield lambda: dcp.paged_attention(q, k, v, table, seq, **kw)
+        yield lambda: dcp.paged_attention_pack(q, k, v, table, seq, 2, **kw)
+        yield lambda: dcp.dcp_kv_append(new, new, k, v, table, seq, starts, **kw)
+        yield lambda: dcp.dcp_kv_weights(logits, lse, seq, w, **kw)
+        yield lambda: dcp.kv_evict(w, k, v, table, seq, new_table, 20, 4, k_out=out, v_out=out.clone(), **kw)
+
+    for kw in (dict(interleave=(1 << 32) + 1), dict(num_shards=(1 << 32) + 1), dict(shard=1 << 32)):
+        for call in calls(**kw):
+            with pytest.raises(ValueError, match="32-bit"):
+                call()
+    for call in calls():
+        call()
+    with pytest.raises(dcp.DCPError, match="overlap"):
+        dcp.paged_attention(q, k, v, table, seq, logits=logits[:, :1].expand(2, 4, 64))
+    with pytest.raises(dcp.DCPError, match="overlap"):
+        dcp.dcp_kv_weights(logits, lse, seq, w[:1].expand(2, 2, 64))
+    with pytest.raises(dcp.DCPError, match="overlap"):
+        dcp.dcp_kv_append(new, new, k[:, :, :1].expand_as(k), v, table, seq, starts)
+    with pytest.raises(dcp.DCPError, match="overlap"):
+        dcp.kv_evict(w, k, v, table, seq, new_table, 20, 4, k_out=out[:1].expand_as(out), v_out=out)
+
+
 # ---- all of it together -----------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype,layout", [("bf16", "slots"), ("fp32", "heads")])
 def test_decode_loop_of_three_ranks(dtype, layout):

@@ -151,6 +151,22 @@ def test_evict_rejections(lib):
         assert evict(lib, **bad) == MISALIGNED, bad
 
 
+def test_overlapping_outputs(lib):
+    """Rows that a call writes must be apart; rows that it only reads may be the same."""
+    for bad in (dict(k_stride_page=0), dict(v_stride_slot=0), dict(k_stride_head=120), dict(v_stride_head=0)):
+        assert append(lib, **bad) == INVALID, bad
+        assert "overlap" in dcp.dcp_last_error()
+        assert evict(lib, dst=cache(**bad)) == INVALID, bad
+        assert "overlap" in dcp.dcp_last_error()
+        assert evict(lib, B=0, **bad) == OK and attend(lib, B=0, **bad) == OK
+    # dimensions of one entry
+    assert append(lib, R=0, num_pages=1, k_stride_page=0, page_size=1, v_stride_slot=0, heads=1, k_stride_head=0) == OK
+    for call, bad in ((weigh, dict(wb=0)), (weigh, dict(wh=63)), (evict, dict(nb=0)), (evict, dict(nh=31)),
+                      (attend, dict(logits=A, cap=64, lb=512, lh=63)), (attend, dict(logits=A, cap=64, lb=0, lh=64))):
+        assert call(lib, **bad) == INVALID, bad
+        assert "overlap" in dcp.dcp_last_error()
+
+
 def tensors():
     k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
     return dict(q=torch.zeros(3, 8, 64, dtype=torch.bfloat16), k=k, v=k.clone(),
