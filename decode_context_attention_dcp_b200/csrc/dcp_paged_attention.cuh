@@ -143,6 +143,7 @@ struct AttentionShape {
     static constexpr int kQueries = kHalfType ? ST * kQuery : 2 * kQuery;
     static constexpr bool kQueryRegs = NH * DP * kBytes * kBytes <= 1024;  // at most 32 registers
     static constexpr size_t kSmem = (size_t)NW * ST * kStage + kQueries;
+    static_assert(ST > 1 || !kHalfType, "16-bit types copy the query with the first tile, ahead of the loop");
     static_assert(kStage >= 16 * DP * 4, "a stage holds 16 fp32 rows (the merge)");
 };
 
@@ -654,9 +655,9 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[h][e] = x1[h][e] = x2[h][e] = 0.f;
-                // a panel (32 elements) at a time: unrolled up to D = 128 (66 against 69 us for 24 requests of 3000),
-                // rolled above (176 against 199 us)
-                auto panel = [&](int pn) {
+                // all of it unrolled: 3% faster than a loop over panels at D = 64 with 64 heads on 4, no slower elsewhere
+#pragma unroll
+                for (int pn = 0; pn < S::kPanels; ++pn) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int ks = 4 * pn + i;
@@ -694,13 +695,6 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                                 for (int e = 0; e < 4; ++e) x[h][e] += part[h][e];
                         }
                     }
-                };
-                if constexpr (DP <= 128) {
-#pragma unroll
-                    for (int pn = 0; pn < S::kPanels; ++pn) panel(pn);
-                } else {
-#pragma unroll 1
-                    for (int pn = 0; pn < S::kPanels; ++pn) panel(pn);
                 }
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
@@ -806,7 +800,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                             const float odd = __shfl_sync(0xffffffffu, w[h][2 * f + 1], from);
                             tf32_split(g & 1 ? odd : even, wh[h][f][e], wl[h][f][e]);
                         }
-// the tile's products in sums of their own, added to o in fp32: the product units cut what they
+                // the tile's products in sums of their own, added to o in fp32: the product units cut what they
                 // add to a long sum, which over thousands of positions would be seen (1.6e-6 of the result)
 #pragma unroll
                 for (int j = 0; j < DP / 16; ++j) {
@@ -1204,7 +1198,12 @@ int32_t launch_attention(const dcp::AttentionArgs &a, cudaStream_t stream) {
     return launch_stream<S>(a, maps, stream);
 }
 
-// The shape for a group of G query heads per key head and D elements.
+// The shape for a group of G query heads per key head and D elements, as measured.  fp32 above D = 64 has
+// room for 12 (D = 256: 6) warps of one stage or half as many of two, and computes for so long that the
+// number of warps counts: a stage is not refilled while its warp computes, but the other warps' copies
+// run.  24 requests of 3000, 12 heads on 4, one stage against two: D = 128 59.7 / 65.6 us, D = 256 129 / 176;
+// 64 heads on 4, D = 128: 79 / 92.  For 16-bit types of D = 256 the exchange does not pay (54.5 / 55 us; 64 heads
+// on 4: 89 / 59).
 template <class T, class F>
 auto with_shape(int32_t group, int32_t head_dim, F &&f) {
     using dcp::AttentionShape;
@@ -1222,8 +1221,8 @@ auto with_shape(int32_t group, int32_t head_dim, F &&f) {
         if (head_dim <= 64)
             return group <= 8 ? f(AttentionShape<T, 64, 1, 4, 2, 3>{}) : f(AttentionShape<T, 64, 2, 4, 2, 3>{});
         if (head_dim <= 128)
-            return group <= 8 ? f(AttentionShape<T, 128, 1, 6, 2, 1>{}) : f(AttentionShape<T, 128, 2, 6, 2, 1>{});
-        return f(AttentionShape<T, 256, 1, 3, 2, 1>{});
+            return group <= 8 ? f(AttentionShape<T, 128, 1, 4, 1, 3>{}) : f(AttentionShape<T, 128, 2, 6, 1, 2>{});
+        return f(AttentionShape<T, 256, 1, 3, 1, 2>{});
     }
 }
 
