@@ -239,6 +239,13 @@ __device__ __forceinline__ void iter_next(const AttentionArgs &a, TileIter &it) 
 }
 
 // ---- results ------------------------------------------------------------------------------------
+// Word offset of the result row of (b, h).
+__device__ __forceinline__ int64_t result_row(const AttentionArgs &a, int b, int h) {
+    if (!a.pack_hr) return ((int64_t)b * a.H + h) * a.kv.data_w;
+    const int rank = (int)a.pack_div.div((uint32_t)h);
+    return (((int64_t)rank * a.B + b) * a.pack_hr + (h - rank * a.pack_hr)) * (a.kv.data_w + 1);
+}
+
 // Four columns of the result row of (b, h), and with column 0 its LSE; sum == 0 is an empty row.
 template <class T>
 __device__ __forceinline__ void write_result(const AttentionArgs &a, int b, int h, int col, const float4 &o, float m,
@@ -246,11 +253,7 @@ __device__ __forceinline__ void write_result(const AttentionArgs &a, int b, int 
     const bool empty = sum == 0.f;
     const float r = empty ? 0.f : 1.f / sum;
     const float f[4] = {empty ? 0.f : o.x * r, empty ? 0.f : o.y * r, empty ? 0.f : o.z * r, empty ? 0.f : o.w * r};
-    int64_t off = ((int64_t)b * a.H + h) * a.kv.data_w;
-    if (a.pack_hr) {
-        const int rank = (int)a.pack_div.div((uint32_t)h);
-        off = (((int64_t)rank * a.B + b) * a.pack_hr + (h - rank * a.pack_hr)) * (a.kv.data_w + 1);
-    }
+    const int64_t off = result_row(a, b, h);
     const int w = col / T::kPerWord;
     if (w < a.kv.data_w) {  // a row is a whole number of 16-byte chunks: four columns are in or out together
         uint32_t *p = a.out + off + w;
@@ -282,7 +285,110 @@ __device__ __forceinline__ void write_result(const AttentionArgs &a, int b, int 
     }
 }
 
+// Whether a row's sums call for mend_columns: some are not finite although its weights are (m and sum: their
+// maximum and sum; a row without weights is written as an empty one).
+__device__ __forceinline__ bool needs_mending(const float4 &o, float m, float sum) {
+    const float zero = fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f)));
+    return zero != 0.f && isfinite(m) && isfinite(sum) && sum > 0.f;
+}
+
+// What non-finite values make of four columns of the result row of (b, h), which write_result has
+// written: the sum of their products with the weights 2^(x - m) as IEEE forms it (inf, -inf or NaN).  The
+// stream's products cannot say: a weight enters them as two parts, of which the second may be 0 or
+// negative (0 inf and inf - inf are NaN where the formula gives inf).  Columns whose values are all finite
+// stay as they are.  One thread reads the values of its columns again, four positions at a time until all
+// four columns are NaN, and a key row for each value that is not finite (its weight may be 0, which
+// makes NaN of an infinity): a path that finite caches never take.
+template <class T>
+__device__ __noinline__ void mend_columns(const AttentionArgs &a, int b, int h, int col, float m) {
+    constexpr int PW = T::kPerWord, U = 4;
+    if (col / PW >= a.kv.data_w) return;
+    const int n = local_length(a.sh, a.seq_lens[b], a.kv.capacity), j = h / a.group;
+    const int32_t *table = a.kv.table + b * a.kv.table_stride;
+    const uint32_t *q = a.q + b * a.q_sb_w + h * a.q_sh_w;
+    const uint32_t *values = a.kv.v + j * a.kv.v_head_w + col / PW, *keys = a.kv.k + j * a.kv.k_head_w;
+    float r[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int p0 = 0; p0 < n && !(isnan(r[0]) && isnan(r[1]) && isnan(r[2]) && isnan(r[3])); p0 += U) {
+        float v[U][4];
+        int64_t key[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.f;
+            key[u] = 0;
+            int64_t page;
+            uint32_t slot;
+            if (p0 + u < n && locate(a.kv, table, (uint32_t)(p0 + u), page, slot)) {
+                const uint32_t *at = values + page * a.kv.v_page_w + slot * a.kv.v_slot_w;
+#pragma unroll
+                for (int i = 0; i < 4 / PW; ++i) T::decode(__ldg(at + i), &v[u][PW * i]);
+                key[u] = page * a.kv.k_page_w + slot * a.kv.k_slot_w;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            bool counts = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) counts = counts || !(isfinite(v[u][e]) || isnan(r[e]));
+            if (!counts) continue;
+            float x = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < a.kv.data_w; ++i) {
+                float qf[2], kf[2];
+                T::decode(__ldg(q + i), qf);
+                T::decode(__ldg(keys + key[u] + i), kf);
+#pragma unroll
+                for (int e = 0; e < PW; ++e) x = fmaf(qf[e], kf[e], x);
+            }
+            const float w = exp2_fast(x * (a.scale * kLog2e) - m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!isfinite(v[u][e])) r[e] += w * v[u][e];  // never 0
+        }
+    }
+    uint32_t *to = a.out + result_row(a, b, h) + col / PW;
+#pragma unroll
+    for (int i = 0; i < 4 / PW; ++i) {
+        float f[2];
+        T::decode(to[i], f);
+#pragma unroll
+        for (int e = 0; e < PW; ++e)
+            if (r[PW * i + e] != 0.f) f[e] = r[PW * i + e];
+        to[i] = T::encode(f);
+    }
+}
+
 __device__ __forceinline__ float finite_or_zero_max(float m) { return m == -INFINITY ? 0.f : m; }
+
+// mend_columns for the requests that a CTA's share of `count` tiles holds whole; it begins at tile
+// where[2] of request where[0] and key head and head block where[1].
+template <class T, int TILE, int HEADS>
+__device__ __noinline__ void mend_share(const AttentionArgs &a, const int *where, int64_t count) {
+    TileIter it;
+    it.b = where[0];
+    it.kvh = where[1] / a.row_blocks;
+    it.rb = where[1] - it.kvh * a.row_blocks;
+    it.t = where[2];
+    it.next_seq = a.seq_lens[it.b];
+    iter_request<TILE>(a, it);
+    while (count > 0) {
+        const int left = it.nt - it.t, head0 = it.rb * HEADS, chunks = a.kv.data_w * T::kPerWord / 4;
+        const int rows = it.t == 0 && count >= left ? min(HEADS, a.group - head0) : 0;
+        for (int x = threadIdx.x; x < rows * chunks; x += blockDim.x) {
+            const int r = x / chunks, c = x - r * chunks, h = it.kvh * a.group + head0 + r;
+            const int64_t row = result_row(a, it.b, h);
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4 / T::kPerWord; ++i) T::decode(a.out[row + c * 4 / T::kPerWord + i], f + T::kPerWord * i);
+            const float lse = a.pack_hr ? __uint_as_float(a.out[row + a.kv.data_w]) : a.lse[(int64_t)it.b * a.H + h];
+            // 2^(x - lse) are the weights divided by their sum
+            if (needs_mending(make_float4(f[0], f[1], f[2], f[3]), lse, 1.f))
+                mend_columns<T>(a, it.b, h, c * 4, a.base_e ? lse * kLog2e : lse);
+        }
+        count -= left;
+        it.t = it.nt - 1;
+        iter_next<TILE>(a, it);
+    }
+}
 
 // ---- the stream ---------------------------------------------------------------------------------
 // Tensor maps of the pools: [pages, slots, heads, D].
@@ -298,6 +404,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[NW];
     __shared__ int s_where[3];
+    __shared__ int s_mend;                         // a finished request needs mend_columns
     __shared__ float2 s_stat[NW][S::kHeads];       // maximum and sum of each warp's heads at a merge
     __shared__ uint32_t s_held[ST][NW];            // bit r: position r of the warp's stage counts
     __shared__ uint2 s_row[NW][WP];                // cp.async: offsets of the K and V rows being copied
@@ -307,6 +414,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");
+    if (!CLUSTER && tid == 0) s_mend = 0;
     constexpr bool TENSOR = S::BOX > 0;
     if (TENSOR && lane == 0) {
         for (int st = 0; st < ST; ++st) mbar_init(&s_full[warp][st], 1);
@@ -893,6 +1001,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                         if (c == 0) s_part[h0 * 8 + r] = make_float2(top, total);
                     } else if (whole) {
                         write_result<T>(a, cp.b, cp.kvh * a.group + head0 + h0 * 8 + r, c * 4, acc, top, total);
+                        if (needs_mending(acc, top, total)) s_mend = 1;
                     } else {
                         const int64_t at = part * S::kHeads + h0 * 8 + r;
                         *reinterpret_cast<float4 *>(ws.rows + at * DP + c * 4) = acc;
@@ -945,9 +1054,13 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                 acc.z = fmaf(v[k].z, f, acc.z);
                 acc.w = fmaf(v[k].w, f, acc.w);
             }
-            write_result<T>(a, ld0_b, ld0_kvh * a.group + head0 + r, c * 4, acc, top, total);
+            const int h = ld0_kvh * a.group + head0 + r;
+            write_result<T>(a, ld0_b, h, c * 4, acc, top, total);
+            if (needs_mending(acc, top, total)) mend_columns<T>(a, ld0_b, h, c * 4, top);
         }
         cluster.sync();  // no CTA leaves while another reads its shared memory
+    } else if (s_mend) {  // the same for all threads: read after the last merge's barrier
+        mend_share<T, TILE, S::kHeads>(a, s_where, count);
     }
     if (TENSOR && late) {  // copies may still be on their way into this CTA's shared memory: wait, bounded
         const uint64_t t0 = global_ns();
@@ -1093,7 +1206,9 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
             t.z = fmaf(v.z, f, t.z);
             t.w = fmaf(v.w, f, t.w);
         }
-        write_result<T>(a, spill.y, spill.z * a.group + spill.w * HEADS + r0 + r, col * 4, t, top, total);
+        const int h = spill.z * a.group + spill.w * HEADS + r0 + r;
+        write_result<T>(a, spill.y, h, col * 4, t, top, total);
+        if (needs_mending(t, top, total)) mend_columns<T>(a, spill.y, h, col * 4, top);
     }
 }
 
