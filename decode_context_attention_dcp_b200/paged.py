@@ -277,7 +277,8 @@ def dcp_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tenso
 
     Tokens query_start_loc[r] <= t < query_start_loc[r + 1] are the last ones of request r's
     seq_lens[r] positions (new tokens included).  Only the positions that this rank holds are
-    written; tokens outside every request are skipped."""
+    written; tokens outside every request are skipped.  Two tokens that land in the same slot (requests
+    that share the page they append to) leave a mixture of their rows there."""
     if stream is None and _done(_binding().append(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
                                                   query_start_loc, shard, num_shards, interleave)):
         return

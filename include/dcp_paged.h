@@ -152,8 +152,9 @@ int32_t dcp_paged_attention_pack(const dcp_paged_kv *kv, const void *q, const in
  * token t has position seq_lens[r] - (query_start_loc[r+1] - t).  This rank writes those whose
  * position it holds (blocks of `interleave` positions dealt to num_shards ranks); the others, tokens
  * outside every request, with a negative position, past max_pages pages or in a page outside
- * the pool are skipped.  Bit-exact copies.  Two tokens of one call that land in the same slot
- * (pages shared between requests that both append) leave either token's row there.
+ * the pool are skipped.  Bit-exact copies.  Where two tokens of one call land in the same slot (pages
+ * shared between requests that both append), each element of its rows is one of the two tokens', without
+ * an order: the key row may hold parts of both, and the value row another mixture.
  *
  * k_new, v_new  [T, heads, head_dim] of kv->dtype; element (t, h, d) at t*stride_t + h*stride_h + d.
  * seq_lens      [num_reqs] int32, device: lengths over all shards, the new tokens included.

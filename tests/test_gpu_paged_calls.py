@@ -1,0 +1,40 @@
+"""Calls of the paged cache that the documentation allows and that lie off the usual path: the same slot
+named twice, lengths that name nothing, arrays wider than their content."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import decode_context_attention_dcp_b200 as dcp
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R", [2, 500])
+def test_tokens_appended_to_the_same_slot(dtype, R):
+    """Requests in pairs that share their page: every element of the slot is one of the two tokens', nothing else
+    is written, and requests of their own pages get their token whole."""
+    page, heads, D = 4, 3, 64
+    k = torch.full((R, page, heads, D), -1.0, dtype=dtype, device="cuda")
+    v = torch.full_like(k, -2.0)
+    # values below 256, so that bf16 tells tokens of a pair apart
+    token = torch.arange(R, device="cuda") % 100 + 1
+    k_new = token.to(dtype)[:, None, None].expand(R, heads, D).contiguous()
+    v_new = (token + 100).to(dtype)[:, None, None].expand(R, heads, D).contiguous()
+    own = torch.arange(R, device="cuda") % 10 >= 8  # the last pair of ten keep their own pages
+    table = torch.where(own, torch.arange(R, device="cuda"), torch.arange(R, device="cuda") // 2 * 2)
+    dcp.dcp_kv_append(k_new, v_new, k, v, table.to(torch.int32)[:, None], i32([2] * R), i32(list(range(R + 1))))
+    for pool, new, fill in ((k, k_new, -1.0), (v, v_new, -2.0)):
+        assert (pool[:, [0, 2, 3]] == fill).all()
+        slot = pool[:, 1]
+        first = torch.arange(R, device="cuda") // 2 * 2
+        shared, partner = ~own & (first == torch.arange(R, device="cuda")), (first + 1).clamp(max=R - 1)
+        assert torch.equal(slot[own], new[own])
+        either = (slot == new) | (slot == new[partner])
+        assert either[shared].all()
+        assert (slot[~own & ~shared] == fill).all()
