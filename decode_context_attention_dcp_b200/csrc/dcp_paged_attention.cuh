@@ -1348,7 +1348,8 @@ int32_t paged_attention(const dcp::AttentionArgs &a, cudaStream_t stream) {
     });
 }
 
-inline cudaError_t attention_timeouts(unsigned long long &count, int32_t reset) {
+// Internal linkage: each translation unit has its own counter and needs its own reader of it.
+static cudaError_t attention_timeouts(unsigned long long &count, int32_t reset) {
     unsigned long long v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, dcp::g_wait_timeouts, sizeof(v));
     if (e == cudaSuccess && reset) {
