@@ -91,6 +91,7 @@ struct AttentionArgs {
     uint32_t unit;
     uint32_t k_page_u, k_slot_u, k_head_u;
     uint32_t v_page_u, v_slot_u, v_head_u;
+    uint32_t stall_bytes;  // added to the bytes that a wait for tensor copies expects: 0, except in the timeout check
     Shards sh;
     const uint32_t *q;
     const int32_t *seq_lens;
@@ -107,6 +108,7 @@ struct AttentionArgs {
     FastDiv pack_div;
     float scale;
     int32_t base_e;
+    uint64_t wait_limit_ns;  // limit of a wait for tensor copies (kWaitLimitNs)
 };
 
 struct AppendArgs {

@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include "dcp_paged.cuh"
+#include "dcp_testing.h"
 
 namespace {
 
@@ -143,7 +144,8 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
                   float *lse, float *logits, int64_t B, int64_t H, int32_t world_size, int64_t q_stride_b,
                   int64_t q_stride_h, int64_t logits_stride_b, int64_t logits_stride_h, int64_t logits_cap,
                   float scale, int32_t shard, int32_t num_shards, int32_t interleave, int32_t is_lse_base_on_e,
-                  void *workspace, int64_t workspace_bytes, void *cuda_stream) {
+                  void *workspace, int64_t workspace_bytes, void *cuda_stream,
+                  uint64_t wait_limit_ns = dcp::kWaitLimitNs, uint32_t stall_bytes = 0) {
     dcp::AttentionArgs a{};
     int32_t st = check_cache(fn, kv, B != 0, false, a.kv);
     if (st == DCP_OK) st = check_shards(fn, shard, num_shards, interleave, a.sh);
@@ -208,6 +210,8 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
     a.pack_div = fast_div(world_size ? (uint64_t)(H / world_size) : 1);
     a.scale = scale;
     a.base_e = is_lse_base_on_e != 0;
+    a.stall_bytes = stall_bytes;
+    a.wait_limit_ns = wait_limit_ns;
     const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     switch (kv->dtype) {
         case DCP_BF16: return dcp_host::paged_attention_bf16(a, stream);
@@ -249,6 +253,15 @@ int32_t dcp_paged_attention_pack(const dcp_paged_kv *kv, const void *q, const in
     return attention(fn, kv, q, seq_lens, send_buf, nullptr, logits, B, H, world_size, q_stride_b, q_stride_h,
                      logits_stride_b, logits_stride_h, logits_cap, scale, shard, num_shards, interleave,
                      is_lse_base_on_e, workspace, workspace_bytes, cuda_stream);
+}
+
+int32_t dcp_testing_paged_attention_stalled(const dcp_paged_kv *kv, const void *q, const int32_t *seq_lens,
+                                            void *result, float *lse, int64_t B, int64_t H, int64_t q_stride_b,
+                                            int64_t q_stride_h, float scale, void *workspace, int64_t workspace_bytes,
+                                            void *cuda_stream) {
+    return attention("dcp_testing_paged_attention_stalled", kv, q, seq_lens, result, lse, nullptr, B, H, 0, q_stride_b,
+                     q_stride_h, 0, 0, 0, scale, 0, 1, 1, 1, workspace, workspace_bytes, cuda_stream,
+                     20000000ull, 16u);
 }
 
 int32_t dcp_kv_append(const dcp_paged_kv *kv, const void *k_new, const void *v_new, const int32_t *seq_lens,

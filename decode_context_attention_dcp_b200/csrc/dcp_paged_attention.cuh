@@ -516,6 +516,12 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     };
     next_page();
     int ld_query = 0, ld_stage = 0;
+    // Tensor copies: the lane, or kLate once a wait of it ran out.  It then neither copies, arms nor waits any
+    // more (lane 0 must not arm a barrier again whose phase is not complete); the result is not valid.
+    // Lanes need not agree: without the copies of some a phase stays incomplete, and the next wait
+    // runs out for the others too.
+    constexpr int kLate = 32;
+    int copier = lane;
 
     // cp.async: one warp-wide copy covers kRowsPerCopy rows (or a 32-chunk part of one)
     constexpr int kRowsPerCopy = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;
@@ -550,13 +556,13 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
 #pragma unroll
                 for (int r = 0; r < kGroups; ++r)
                     if (!((votes >> (r * S::kPanels)) & 1u)) bits &= ~(((1u << S::BOX) - 1u) << (r * S::BOX));
-                if (lane == 0) {
+                if (copier == 0) {
                     s_held[ld_stage][warp] = bits;
-                    mbar_arrive_expect_tx(&s_full[warp][ld_stage], S::kStage);
+                    mbar_arrive_expect_tx(&s_full[warp][ld_stage], S::kStage + a.stall_bytes);
                 }
                 __syncwarp();
                 // a page outside the pool, or past the length (-1), reads zeros
-                if (lane < kBoxes) {
+                if (copier < kBoxes) {
                     const bool is_v = lane >= kBoxes / 2;
                     tensor_copy(stages + ld_stage * S::kStage + (is_v ? S::kHalf : 0) + box_panel * S::kPanel +
                                     box_group * (S::BOX * 128),
@@ -621,7 +627,6 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     // Places of this lane in a stage: ldmatrix rows of K (16-bit) or its floats of K (fp32), and of V.  Of
     // chunk c = 2 j + e the part that depends on j mod 4 is in these, the rest is panel j / 4.
     uint32_t phases = 0;   // bit st: parity of stage st's next arrival
-    bool late = false;     // a wait ran out: nothing more is waited for, the result is not valid
     uint32_t k_at[4], v_at[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -707,9 +712,10 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
             const uint32_t stage = stages + cp_stage * S::kStage;
             const uint32_t held = s_held[cp_stage][warp];
             if constexpr (TENSOR) {
-                if (!late && !mbar_wait_bounded(&s_full[warp][cp_stage], (phases >> cp_stage) & 1u, kWaitLimitNs)) {
-                    late = true;
-                    if (lane == 0) atomicAdd(&g_wait_timeouts, 1ull);
+                if (copier != kLate &&
+                    !mbar_wait_bounded(&s_full[warp][cp_stage], (phases >> cp_stage) & 1u, a.wait_limit_ns)) {
+                    copier = kLate;
+                    if (lane == __ffs(__activemask()) - 1) atomicAdd(&g_wait_timeouts, 1ull);
                 }
                 phases ^= 1u << cp_stage;
                 if (held != (1u << WP) - 1u) {
@@ -1062,9 +1068,9 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     } else if (s_mend) {  // the same for all threads: read after the last merge's barrier
         mend_share<T, TILE, S::kHeads>(a, s_where, count);
     }
-    if (TENSOR && late) {  // copies may still be on their way into this CTA's shared memory: wait, bounded
+    if (TENSOR && copier == kLate) {  // copies may still be on their way into this CTA's shared memory: wait, bounded
         const uint64_t t0 = global_ns();
-        for (uint32_t spin = 0; spin < (1u << 26) && global_ns() - t0 < kWaitLimitNs; ++spin) {
+        for (uint32_t spin = 0; spin < (1u << 26) && global_ns() - t0 < a.wait_limit_ns; ++spin) {
         }
     }
 }

@@ -1,7 +1,7 @@
 /*
- * dcp_testing.h -- test hooks of libdcpcombine.so: one makes the timeout path of the pack
- * kernels' bounded waits run, so that a test can check it without faulting or hanging a
- * GPU; one reports the launch shape the host picks for a split-layout combine, so that the
+ * dcp_testing.h -- test hooks of libdcpcombine.so: two make the timeout paths of the pack
+ * kernels' and of the paged attention's bounded waits run, so that a test can check them without
+ * faulting or hanging a GPU; one reports the launch shape the host picks for a split-layout combine, so that the
  * shape rules can be checked without a GPU; two report which pack kernel ran and the tensor
  * pack's tile shape.  Not part of the combine; no page has a counterpart.
  */
@@ -9,6 +9,8 @@
 #define DCP_TESTING_H
 
 #include <stdint.h>
+
+#include "dcp_paged.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -26,6 +28,19 @@ int32_t dcp_testing_pack_stalled(const void *cp_attn_out, const float *cp_attn_l
                                  int64_t B, int64_t H, int64_t D, int32_t world_size, int32_t dtype,
                                  int64_t out_stride_b, int64_t out_stride_h, int64_t lse_stride_b,
                                  void *cuda_stream);
+
+/*
+ * dcp_paged_attention (num_shards 1, base e, no logits; same validation and status codes) with two
+ * changes: each wait for tensor copies expects 16 bytes that never arrive, and gives up after 20 ms instead
+ * of one second.  Every copy still completes; only the wait runs out.  Each warp that waits is
+ * counted once in dcp_wait_timeouts, then neither copies nor waits any more; result and lse are not valid.
+ * The kernel returns normally, and the device stays usable.  Calls that use no tensor copies (page sizes
+ * that are no multiple of 8) are not changed.
+ */
+int32_t dcp_testing_paged_attention_stalled(const dcp_paged_kv *kv, const void *q, const int32_t *seq_lens,
+                                            void *result, float *lse, int64_t B, int64_t H, int64_t q_stride_b,
+                                            int64_t q_stride_h, float scale, void *workspace, int64_t workspace_bytes,
+                                            void *cuda_stream);
 
 /*
  * The shape the host picks for a split-layout combine of N shards whose rows are `chunks`
