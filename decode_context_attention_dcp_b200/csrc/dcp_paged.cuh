@@ -152,6 +152,10 @@ int32_t paged_attention_fp32(const dcp::AttentionArgs &a, cudaStream_t stream);
 int64_t attention_workspace_bf16(int32_t group, int32_t head_dim);
 int64_t attention_workspace_fp16(int32_t group, int32_t head_dim);
 int64_t attention_workspace_fp32(int32_t group, int32_t head_dim);
+// Resident and assumed CTAs per SM (dcp_testing_paged_attention_resident).
+int32_t attention_resident_bf16(int32_t group, int32_t head_dim, int box, bool cluster, int32_t *out);
+int32_t attention_resident_fp16(int32_t group, int32_t head_dim, int box, bool cluster, int32_t *out);
+int32_t attention_resident_fp32(int32_t group, int32_t head_dim, int box, bool cluster, int32_t *out);
 int32_t kv_append(const dcp::AppendArgs &a, cudaStream_t stream);
 int32_t kv_weights(const dcp::WeightsArgs &a, cudaStream_t stream);
 int32_t kv_evict(const dcp::EvictArgs &a, cudaStream_t stream);

@@ -264,6 +264,18 @@ int32_t dcp_testing_paged_attention_stalled(const dcp_paged_kv *kv, const void *
                      20000000ull, 16u);
 }
 
+int32_t dcp_testing_paged_attention_resident(int32_t group, int32_t head_dim, int32_t dtype, int32_t page_size,
+                                             int32_t cluster, int32_t *out) {
+    if (group < 1 || head_dim < 1 || head_dim > DCP_MAX_PAGED_DIM || page_size < 1 || elem_size(dtype) == 0 || !out)
+        return fail(DCP_ERR_INVALID_ARG, "dcp_testing_paged_attention_resident: argument out of range");
+    const int box = page_size % 16 == 0 ? 16 : page_size % 8 == 0 ? 8 : 0;
+    switch (dtype) {
+        case DCP_BF16: return dcp_host::attention_resident_bf16(group, head_dim, box, cluster != 0, out);
+        case DCP_FP16: return dcp_host::attention_resident_fp16(group, head_dim, box, cluster != 0, out);
+        default: return dcp_host::attention_resident_fp32(group, head_dim, box, cluster != 0, out);
+    }
+}
+
 int32_t dcp_kv_append(const dcp_paged_kv *kv, const void *k_new, const void *v_new, const int32_t *seq_lens,
                       const int32_t *query_start_loc, int64_t T, int32_t num_reqs, int64_t k_stride_t,
                       int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h, int32_t shard, int32_t num_shards,

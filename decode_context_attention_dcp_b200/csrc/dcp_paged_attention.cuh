@@ -143,6 +143,13 @@ struct AttentionShape {
     static constexpr int kQueries = kHalfType ? ST * kQuery : 2 * kQuery;
     static constexpr bool kQueryRegs = NH * DP * kBytes * kBytes <= 1024;  // at most 32 registers
     static constexpr size_t kSmem = (size_t)NW * ST * kStage + kQueries;
+    // Static shared memory, in units of the dynamic part's alignment: the warps' scratch, held bits, barriers
+    // (tensor copies), and the scan and place (even shares) or the heads' sums (clusters).  CTAS blocks fit an
+    // SM's 228 KB, of which each block takes 1 KB for the system.
+    static constexpr int kScratch = 8 * (WP > kHeads ? WP : kHeads);  // per warp
+    static constexpr int kEnds = 8 * NW + 16 > 8 * kHeads ? 8 * NW + 16 : 8 * kHeads;
+    static constexpr int kStatic = NW * kScratch + 4 * ST * NW + (BOX ? 8 * NW * ST : 0) + kEnds;
+    static_assert((kSmem + (kStatic + 1023) / 1024 * 1024 + 1024) * CTAS <= 228 * 1024, "CTAS blocks per SM");
     static_assert(ST > 1 || !kHalfType, "16-bit types copy the query with the first tile, ahead of the loop");
     static_assert(kStage >= 16 * DP * 4, "a stage holds 16 fp32 rows (the merge)");
 };
@@ -405,9 +412,12 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     __shared__ int64_t s_scan[NW];
     __shared__ int s_where[3];
     __shared__ int s_mend;                         // a finished request needs mend_columns
-    __shared__ float2 s_stat[NW][S::kHeads];       // maximum and sum of each warp's heads at a merge
+    // Each warp's: at a merge the maximum and sum of its heads; with cp.async, between merges, the offsets of the
+    // K and V rows that it is copying.
+    __shared__ __align__(8) uint8_t s_scratch[NW][S::kScratch];
+    auto s_stat = [&](int w) { return reinterpret_cast<float2 *>(s_scratch[w]); };
+    auto s_row = [&](int w) { return reinterpret_cast<uint2 *>(s_scratch[w]); };
     __shared__ uint32_t s_held[ST][NW];            // bit r: position r of the warp's stage counts
-    __shared__ uint2 s_row[NW][WP];                // cp.async: offsets of the K and V rows being copied
     __shared__ uint64_t s_full[NW][ST];            // tensor copies: a stage's bytes have arrived
     __shared__ float2 s_part[S::kHeads];           // cluster: maximum and sum of this CTA's heads
     namespace cg = cooperative_groups;
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                 const uint32_t bits = votes & ((1u << WP) - 1u);
                 __syncwarp();  // the last tile's offsets have been read
                 if (lane < WP)
-                    s_row[warp][lane] = make_uint2(entry * a.k_page_u + slot * a.k_slot_u + ld.kvh * a.k_head_u,
+                    s_row(warp)[lane] = make_uint2(entry * a.k_page_u + slot * a.k_slot_u + ld.kvh * a.k_head_u,
                                                    entry * a.v_page_u + slot * a.v_slot_u + ld.kvh * a.v_head_u);
                 if (lane == 0) s_held[ld_stage][warp] = bits;
                 __syncwarp();
@@ -582,7 +592,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
 #pragma unroll
                     for (int i = 0; i < WP * S::kChunks / 32; ++i) {
                         const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
-                        const uint2 at = s_row[warp][row0 + my_row];
+                        const uint2 at = s_row(warp)[row0 + my_row];
                         // (row0 + my_row) mod 8 = (row0 mod 8) ^ my_row: my_row < kRowsPerCopy, which divides row0
                         const uint32_t to = dst + (lane_sw ^ ((row0 & 7) << 4));
                         const int more = row0 * 128 + c0 / 8 * S::kPanel;
@@ -593,7 +603,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
 #pragma unroll 1
                     for (int i = 0; i < WP * S::kChunks / 32; ++i) {
                         const int row0 = i / kCopiesPerRow * kRowsPerCopy, c0 = i % kCopiesPerRow * 32;
-                        const uint2 at = s_row[warp][row0 + my_row];
+                        const uint2 at = s_row(warp)[row0 + my_row];
                         const uint32_t to = dst + (lane_sw ^ ((row0 & 7) << 4)) + row0 * 128 + c0 / 8 * S::kPanel;
                         const bool in = ((bits >> (row0 + my_row)) & 1u) && (my_chunk + c0) * 4 < a.kv.data_w;
                         cp_async_or_zero(to, in ? k_base + (uint64_t)at.x * a.unit + c0 * 16 : (const char *)a.kv.k, in);
@@ -964,7 +974,7 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                     float s = sum[h][e];
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                    if (g == 0) s_stat[warp][h * 8 + 2 * t4 + e] = make_float2(m[h][e], s);
+                    if (g == 0) s_stat(warp)[h * 8 + 2 * t4 + e] = make_float2(m[h][e], s);
                 }
 #pragma unroll
             for (int h0 = 0; h0 < NH; h0 += 2) {  // 16 fp32 rows fit this tile's stage, free until the next copy_next
@@ -985,13 +995,13 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
                     const int r = x / (DP / 4), c = x - r * (DP / 4);
                     float top = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) top = fmaxf(top, s_stat[w][h0 * 8 + r].x);
+                    for (int w = 0; w < NW; ++w) top = fmaxf(top, s_stat(w)[h0 * 8 + r].x);
                     const float base = finite_or_zero_max(top);
                     float total = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
-                        const float2 st = s_stat[w][h0 * 8 + r];
+                        const float2 st = s_stat(w)[h0 * 8 + r];
                         const float f = exp2_fast(st.x - base);
                         const float4 v = *reinterpret_cast<const float4 *>(
                             reinterpret_cast<const float *>(smem + (size_t)(w * ST + cp_stage) * S::kStage) + r * DP +
@@ -1364,6 +1374,31 @@ static cudaError_t attention_timeouts(unsigned long long &count, int32_t reset) 
     }
     count += v;
     return e;
+}
+
+// Resident CTAs per SM of the kernel that a call of this shape launches, and how many its launch counts on;
+// box as in launch_attention.
+template <class T>
+int32_t attention_resident(int32_t group, int32_t head_dim, int box, bool cluster, int32_t *out) {
+    return with_shape<T>(group, head_dim, [&](auto shape) {
+        using S = decltype(shape);
+        auto ask = [&](auto kernel, size_t smem) {
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+                return fail(DCP_ERR_CUDA, "attention_resident: cannot reserve shared memory");
+            out[0] = resident_ctas(kernel, S::kThreads, smem);
+            out[1] = S::CTAS;
+            return ok();
+        };
+        auto boxed = [&](auto s) {
+            using B = decltype(s);
+            if constexpr (S::NH <= 2)
+                if (cluster) return ask(dcp::attention_stream_kernel<B, true>, B::kSmem);
+            return ask(dcp::attention_stream_kernel<B, false>, B::kSmem);
+        };
+        return box == 16 ? boxed(typename S::template With<16>{})
+               : box == 8 ? boxed(typename S::template With<8>{})
+                          : boxed(S{});
+    });
 }
 
 template <class T>

@@ -11,6 +11,10 @@ int64_t attention_workspace_bf16(int32_t group, int32_t head_dim) {
     return attention_workspace<dcp::Bf16>(group, head_dim);
 }
 
+int32_t attention_resident_bf16(int32_t group, int32_t head_dim, int box, bool cluster, int32_t *out) {
+    return attention_resident<dcp::Bf16>(group, head_dim, box, cluster, out);
+}
+
 cudaError_t attention_timeouts_bf16(unsigned long long &count, int32_t reset) {
     return attention_timeouts(count, reset);
 }

@@ -3,7 +3,7 @@
  * kernels' and of the paged attention's bounded waits run, so that a test can check them without
  * faulting or hanging a GPU; one reports the launch shape the host picks for a split-layout combine, so that the
  * shape rules can be checked without a GPU; two report which pack kernel ran and the tensor
- * pack's tile shape.  Not part of the combine; no page has a counterpart.
+ * pack's tile shape; one how many blocks of the paged attention an SM holds.  Not part of the combine; no page has a counterpart.
  */
 #ifndef DCP_TESTING_H
 #define DCP_TESTING_H
@@ -41,6 +41,16 @@ int32_t dcp_testing_paged_attention_stalled(const dcp_paged_kv *kv, const void *
                                             void *result, float *lse, int64_t B, int64_t H, int64_t q_stride_b,
                                             int64_t q_stride_h, float scale, void *workspace, int64_t workspace_bytes,
                                             void *cuda_stream);
+
+/*
+ * For the paged attention of `group` query heads per key head, head_dim elements of `dtype` and pages of
+ * page_size slots: out[0] = CTAs of its stream kernel that are resident per SM of the current device,
+ * out[1] = the number that the launch's grid and the workspace count on.  cluster != 0: the kernel of short
+ * calls, where the shape has one.  Returns DCP_OK, DCP_ERR_INVALID_ARG for sizes out of range or a
+ * null `out`, or DCP_ERR_CUDA.
+ */
+int32_t dcp_testing_paged_attention_resident(int32_t group, int32_t head_dim, int32_t dtype, int32_t page_size,
+                                             int32_t cluster, int32_t *out);
 
 /*
  * The shape the host picks for a split-layout combine of N shards whose rows are `chunks`
