@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures
+import contextlib
+import fcntl
 import glob
 import hashlib
 import os
@@ -31,6 +33,8 @@ COMPILE_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2"]
 LINK_FLAGS = ["-shared", "--cudart", "static"]
 BINDING_SOURCE = os.path.join(PKG, "binding", "paged_binding.cpp")
 BINDING = os.path.join(PKG, "_paged_binding.so")
+BINDING_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden"]
+BINDING_LIBS = ["-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-ldl"]
 
 
 def nvcc() -> str:
@@ -78,19 +82,48 @@ def _run(cmd: list[str]) -> None:
         raise RuntimeError(os.path.basename(cmd[0]) + " failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
 
 
+@contextlib.contextmanager
+def _alone():
+    """One process at a time builds in this directory (several ranks make their first call together)."""
+    fd = os.open(PKG, os.O_RDONLY)
+    try:
+        with contextlib.suppress(OSError):  # a file system without locks: the replacements below are atomic all the same
+            fcntl.flock(fd, fcntl.LOCK_EX)
+        yield
+    finally:
+        os.close(fd)
+
+
+def _install(tmp: str, lib: str, digest: str) -> None:
+    """Put a built file and its digest in place, each atomically."""
+    fd, note = tempfile.mkstemp(suffix=".sha256", dir=PKG)
+    with os.fdopen(fd, "w") as fh:
+        fh.write(digest + "\n")
+    os.chmod(note, 0o644)
+    os.replace(tmp, lib)
+    os.replace(note, _digest_file(lib))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every .cu under csrc/ (in parallel, one object each) and link them into one
-    shared library (atomic replace)."""
-    if not force and not stale():
-        return LIBRARY
+    shared library (atomic replace), unless it is there and up to date."""
+    if force or stale(LIBRARY):
+        with _alone():
+            if force or stale(LIBRARY):  # another process may have built it meanwhile
+                _build_library(verbose)
+    return LIBRARY
+
+
+def _build_library(verbose: bool) -> None:
+    digest, compiler = source_digest(), nvcc()
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
     os.close(fd)
     objdir = tempfile.mkdtemp(prefix="dcp_build_")
     srcs = sources()
     objs = [os.path.join(objdir, os.path.basename(src) + ".o") for src in srcs]
-    compiles = [[nvcc(), *ARCH, *COMPILE_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
+    compiles = [[compiler, *ARCH, *COMPILE_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
                 for src, obj in zip(srcs, objs)]
-    link = [nvcc(), *ARCH, *LINK_FLAGS, "-o", tmp, *objs]
+    link = [compiler, *ARCH, *LINK_FLAGS, "-o", tmp, *objs]
     try:
         with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
             for f in [ex.submit(_run, c) for c in compiles]:
@@ -99,59 +132,60 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             for c in compiles + [link]:
                 print(" ".join(c))
-        digest = source_digest()
-        os.replace(tmp, LIBRARY)
-        with open(_digest_file(LIBRARY) + ".tmp", "w") as fh:
-            fh.write(digest + "\n")
-        os.replace(_digest_file(LIBRARY) + ".tmp", _digest_file(LIBRARY))
+        _install(tmp, LIBRARY, digest)
     finally:
         if os.path.exists(tmp):
             os.unlink(tmp)
         shutil.rmtree(objdir, ignore_errors=True)
-    return LIBRARY
 
+
+def _build_binding() -> None:
+    import torch
+
+    digest = binding_digest()
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
+    os.close(fd)
+    cmd = [os.environ.get("CXX", "g++"), *BINDING_FLAGS,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include/torch/csrc/api/include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING_SOURCE,
+           "-L", os.path.join(base, "lib"), *BINDING_LIBS, "-o", tmp]
+    try:
+        _run(cmd)
+        _install(tmp, BINDING, digest)
+    finally:
+        if os.path.exists(tmp):
+            os.unlink(tmp)
 
 
 def binding_digest() -> str:
-    """SHA-256 of the binding's sources and of the Python and torch it is built for."""
+    """SHA-256 of the binding's sources and of the compiler flags, the Python and the torch it is built for."""
     import torch
 
     h = hashlib.sha256()
-    h.update(f"{sys.version} {torch.__version__}".encode())
+    h.update(f"{sys.version} {torch.__version__} {' '.join(BINDING_FLAGS + BINDING_LIBS)}".encode())
     for p in (BINDING_SOURCE, *sorted(glob.glob(os.path.join(INCLUDE, "*.h")))):
         with open(p, "rb") as fh:
             h.update(b"\0" + fh.read())
     return h.hexdigest()
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile the torch binding of the paged calls (atomic replace)."""
-    import torch
+def binding_stale() -> bool:
+    """True unless the binding exists and was built from exactly the current sources, flags and versions."""
+    if not os.path.exists(BINDING) or not os.path.exists(_digest_file(BINDING)):
+        return True
+    with open(_digest_file(BINDING)) as fh:
+        return fh.read().strip() != binding_digest()
 
-    digest = binding_digest()
-    if not force and os.path.exists(BINDING) and os.path.exists(_digest_file(BINDING)):
-        with open(_digest_file(BINDING)) as fh:
-            if fh.read().strip() == digest:
-                return BINDING
-    base = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
-    os.close(fd)
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
-           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include/torch/csrc/api/include"),
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING_SOURCE,
-           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-ldl",
-           "-o", tmp]
-    try:
-        _run(cmd)
-        os.replace(tmp, BINDING)
-        with open(_digest_file(BINDING) + ".tmp", "w") as fh:
-            fh.write(digest + "\n")
-        os.replace(_digest_file(BINDING) + ".tmp", _digest_file(BINDING))
-    finally:
-        if os.path.exists(tmp):
-            os.unlink(tmp)
+
+def build_binding(force: bool = False) -> str:
+    """Compile the torch binding of the paged calls (atomic replace), unless it is there and up to date."""
+    if force or binding_stale():
+        with _alone():
+            if force or binding_stale():
+                _build_binding()
     return BINDING
 
 

@@ -2,8 +2,9 @@
 from __future__ import annotations
 
 import os
-import shutil
 import subprocess
+import sys
+import time
 
 import pytest
 
@@ -22,3 +23,45 @@ def test_each_type_reads_its_own_timeout_counter(tmp_path):
     found = [line for line in symbols.splitlines() if "attention_timeouts(" in line]
     assert found, "the reader was inlined: the test says nothing"
     assert all(line.split()[1] == "t" for line in found), found
+
+
+BUILDER = """
+import os, sys, time
+from decode_context_attention_dcp_b200 import _build
+pkg, what, start = sys.argv[1], sys.argv[2], float(sys.argv[3])
+_build.PKG, _build.LIBRARY = pkg, os.path.join(pkg, "lib.so")
+_build.BINDING = os.path.join(pkg, "binding.so")
+_build.sources = lambda: [os.path.join(pkg, "one.cu")]
+
+def run(cmd):  # a compiler that takes a while
+    with open(os.path.join(pkg, "log"), "a") as fh:
+        fh.write("run\\n")
+    time.sleep(0.3)
+    with open(cmd[cmd.index("-o") + 1], "w") as fh:
+        fh.write("built")
+
+_build._run = run
+time.sleep(max(0.0, start - time.time()))
+getattr(_build, what)()
+"""
+
+
+@pytest.mark.parametrize("what,lib,steps", [("build", "lib.so", 2), ("build_binding", "binding.so", 1)])
+def test_several_processes_build_once(tmp_path, what, lib, steps):
+    """Ranks whose first calls come together: one builds, the others wait, none fails."""
+    (tmp_path / "one.cu").write_text("")
+    start = str(time.time() + 8)
+    code = [sys.executable, "-c", BUILDER, str(tmp_path), what, start]
+    ranks = [subprocess.Popen(code, cwd=_build.ROOT, stderr=subprocess.PIPE, text=True) for _ in range(4)]
+    errors = [p.communicate(timeout=120)[1] for p in ranks]
+    assert [p.returncode for p in ranks] == [0] * 4, errors
+    assert (tmp_path / "log").read_text() == "run\n" * steps
+    assert (tmp_path / lib).read_text() == "built"
+    assert len((tmp_path / (lib + ".sha256")).read_text().strip()) == 64
+    assert sorted(os.listdir(tmp_path)) == sorted(["log", "one.cu", lib, lib + ".sha256"])
+
+
+def test_the_binding_is_rebuilt_for_other_flags(monkeypatch):
+    before = _build.binding_digest()
+    monkeypatch.setattr(_build, "BINDING_FLAGS", [*_build.BINDING_FLAGS, "-DOTHER"])
+    assert _build.binding_digest() != before
