@@ -27,6 +27,7 @@ import ctypes
 import importlib.util
 import math
 import threading
+import warnings
 
 import torch
 
@@ -74,20 +75,35 @@ _native = None
 _lock = threading.Lock()
 
 
+class _NoBinding:
+    """In the place of a binding that could not be built: leaves every call to the code here."""
+    attend = append = weigh = evict = staticmethod(lambda *args: None)
+
+
+def _load_binding():
+    spec = importlib.util.spec_from_file_location(f"{__package__}._paged_binding", _build.build_binding())
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.set_library(_build.build())
+    return module
+
+
 def _binding():
     """The compiled binding (built first if it is missing or older than its source).  Its functions
     make the calls below in the usual case and return None in every other one, where the code here
-    makes the call or says what is wrong with it."""
+    makes the call or says what is wrong with it.  Without a compiler, or a directory to build in, the code
+    here makes all of them."""
     global _native
     if _native is None:
         library()
         with _lock:
             if _native is None:
-                spec = importlib.util.spec_from_file_location(f"{__package__}._paged_binding", _build.build_binding())
-                module = importlib.util.module_from_spec(spec)
-                spec.loader.exec_module(module)
-                module.set_library(_build.build())
-                _native = module
+                try:
+                    _native = _load_binding()
+                except (RuntimeError, OSError, ImportError) as e:
+                    warnings.warn(f"the compiled binding of the paged calls is not available, their host side takes "
+                                  f"10 to 20 us longer per call: {e}", RuntimeWarning, stacklevel=3)
+                    _native = _NoBinding
     return _native
 
 

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import decode_context_attention_dcp_b200 as dcp
+from decode_context_attention_dcp_b200 import paged
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,26 @@ def test_tokens_appended_to_the_same_slot(dtype, R):
         either = (slot == new) | (slot == new[partner])
         assert either[shared].all()
         assert (slot[~own & ~shared] == fill).all()
+
+
+def test_the_same_results_without_the_compiled_binding(monkeypatch):
+    """Every call made by the Python code instead of the binding."""
+    k = torch.randn(12, 16, 2, 64, device="cuda").to(torch.bfloat16)
+    v, q = torch.randn_like(k), torch.randn(2, 4, 64, device="cuda").to(torch.bfloat16)
+    table, seq, starts = i32([[0, 1, 2], [3, 4, 5]]), i32([40, 17]), i32([0, 1, 2])
+    new = torch.randn(2, 2, 64, device="cuda").to(torch.bfloat16)
+
+    def step():
+        kk, vv, w = k.clone(), v.clone(), torch.zeros(2, 2, 48, device="cuda")
+        logits = torch.zeros(2, 4, 48, device="cuda")
+        dcp.dcp_kv_append(new, new + 1, kk, vv, table, seq, starts)
+        out, lse = dcp.paged_attention(q, kk, vv, table, seq, logits=logits)
+        send = dcp.paged_attention_pack(q, kk, vv, table, seq, 2)
+        dcp.dcp_kv_weights(logits, lse, seq, w)
+        kept, lens, weights = dcp.kv_evict(w, kk, vv, table, seq, table + 6, 20, 4)
+        return kk, vv, out, lse, send.view(torch.int16), w, kept, lens, weights
+
+    want = step()
+    monkeypatch.setattr(paged, "_native", paged._NoBinding)
+    for a, b in zip(step(), want):
+        assert torch.equal(a, b)

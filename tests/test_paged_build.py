@@ -5,10 +5,13 @@ import os
 import subprocess
 import sys
 import time
+import warnings
 
 import pytest
+import torch
 
-from decode_context_attention_dcp_b200 import _build
+import decode_context_attention_dcp_b200 as dcp
+from decode_context_attention_dcp_b200 import _build, paged
 
 
 def test_each_type_reads_its_own_timeout_counter(tmp_path):
@@ -27,7 +30,8 @@ def test_each_type_reads_its_own_timeout_counter(tmp_path):
 
 BUILDER = """
 import os, sys, time
-from decode_context_attention_dcp_b200 import _build
+import decode_context_attention_dcp_b200 as dcp
+from decode_context_attention_dcp_b200 import _build, paged
 pkg, what, start = sys.argv[1], sys.argv[2], float(sys.argv[3])
 _build.PKG, _build.LIBRARY = pkg, os.path.join(pkg, "lib.so")
 _build.BINDING = os.path.join(pkg, "binding.so")
@@ -65,3 +69,22 @@ def test_the_binding_is_rebuilt_for_other_flags(monkeypatch):
     before = _build.binding_digest()
     monkeypatch.setattr(_build, "BINDING_FLAGS", [*_build.BINDING_FLAGS, "-DOTHER"])
     assert _build.binding_digest() != before
+
+
+@pytest.mark.parametrize("error", [RuntimeError("g++ failed"), FileNotFoundError("g++"), PermissionError("package"),
+                                   ImportError("undefined symbol")])
+def test_calls_do_without_a_binding_that_cannot_be_built(monkeypatch, error):
+    """One warning, then the Python code makes the calls (or, as here, says what is wrong with one)."""
+    def fail():
+        raise error
+
+    monkeypatch.setattr(paged, "_native", None)
+    monkeypatch.setattr(_build, "build_binding", fail)
+    q, k = torch.zeros(3, 8, 64), torch.zeros(4, 16, 2, 64)
+    args = (q, k, k, torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+    with pytest.warns(RuntimeWarning, match="binding"), pytest.raises(ValueError, match="CUDA"):
+        dcp.paged_attention(*args)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(ValueError, match="CUDA"):
+            dcp.paged_attention(*args)
