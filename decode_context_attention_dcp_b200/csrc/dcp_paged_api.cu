@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <utility>
+
 #include "dcp_paged.cuh"
 #include "dcp_testing.h"
 
@@ -45,9 +47,37 @@ int64_t attention_workspace(int32_t group, int32_t head_dim, int32_t dtype) {
     }
 }
 
-// Rows of `width` elements, n0 times n1 of them, of which neighbours share elements.
-bool rows_overlap(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width) {
-    return (n0 > 1 && s0 < width) || (n1 > 1 && s1 < width);
+// Whether some of the n[0] x n[1] x n[2] rows of `width` elements with strides s share elements.  Layouts
+// in which each dimension steps over all smaller ones, the usual kind, are seen at once; others are
+// looked through, differences of two dimensions against steps of the longest one, as far as that is
+// 2^18 differences (an overlap past those is not found).
+bool rows_overlap(const int64_t (&n)[3], const int64_t (&s)[3], int64_t width) {
+    int by_stride[3] = {0, 1, 2};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (s[by_stride[j]] > s[by_stride[j + 1]]) std::swap(by_stride[j], by_stride[j + 1]);
+    __int128 span = width;
+    bool apart = true;
+    for (int i : by_stride) {
+        if (n[i] <= 1) continue;
+        if (s[i] < width) return true;
+        apart = apart && s[i] >= span;
+        span += (__int128)(n[i] - 1) * s[i];
+    }
+    if (apart || width <= 0) return false;
+    const int c = n[0] >= n[1] && n[0] >= n[2] ? 0 : n[1] >= n[2] ? 1 : 2, a = (c + 1) % 3, b = (c + 2) % 3;
+    const int64_t na = n[a] > 1 ? n[a] : 1, nb = n[b] > 1 ? n[b] : 1;
+    int64_t left = int64_t(1) << 18;
+    for (int64_t i = 0; i < na; ++i)
+        for (int64_t j = 1 - nb; j < nb; ++j) {
+            if (--left < 0) return false;
+            const __int128 at = (__int128)i * s[a] + (__int128)j * s[b], near = at / s[c];
+            for (__int128 k = near - 1; k <= near + 1; ++k) {
+                const __int128 d = at - k * s[c];
+                if ((i || j || k) && -n[c] < k && k < n[c] && -(__int128)width < d && d < width) return true;
+            }
+        }
+    return false;
 }
 
 // `used`: the call reads the block table (it has requests), so its pointers must be there.
@@ -79,8 +109,7 @@ int32_t check_cache(const char *fn, const dcp_paged_kv *kv, bool used, bool writ
     if (used && kv->max_pages > 0 && !kv->block_table) return fail(DCP_ERR_INVALID_ARG, "%s: null block_table", fn);
     if (used && kv->num_pages > 0 && (!kv->k || !kv->v)) return fail(DCP_ERR_INVALID_ARG, "%s: null cache pointer", fn);
     for (int i = 0; written && i < 6; i += 3)
-        if (rows_overlap(kv->num_pages, st[i], kv->page_size, st[i + 1], kv->head_dim) ||
-            rows_overlap(kv->heads, st[i + 2], 1, 0, kv->head_dim))
+        if (rows_overlap({kv->num_pages, kv->page_size, kv->heads}, {st[i], st[i + 1], st[i + 2]}, kv->head_dim))
             return fail(DCP_ERR_INVALID_ARG, "%s: rows of the cache that is written overlap", fn);
     c.k = static_cast<uint32_t *>(kv->k);
     c.v = static_cast<uint32_t *>(kv->v);
@@ -183,7 +212,7 @@ int32_t attention(const char *fn, const dcp_paged_kv *kv, const void *q, const i
         return fail(DCP_ERR_MISALIGNED, "%s: the query and the result must be 16-byte aligned", fn);
     if (!aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(logits, 4))
         return fail(DCP_ERR_MISALIGNED, "%s: seq_lens, lse and logits must be 4-byte aligned", fn);
-    if (logits && rows_overlap(B, logits_stride_b, H, logits_stride_h, logits_cap))
+    if (logits && rows_overlap({B, H, 1}, {logits_stride_b, logits_stride_h, 0}, logits_cap))
         return fail(DCP_ERR_INVALID_ARG, "%s: the rows of logits overlap", fn);
     const int64_t need = attention_workspace((int32_t)(H / kv->heads), kv->head_dim, kv->dtype);
     if (need > 0) {
@@ -276,6 +305,11 @@ int32_t dcp_testing_paged_attention_resident(int32_t group, int32_t head_dim, in
     }
 }
 
+int32_t dcp_testing_rows_overlap(int64_t n0, int64_t n1, int64_t n2, int64_t s0, int64_t s1, int64_t s2,
+                                 int64_t width) {
+    return rows_overlap({n0, n1, n2}, {s0, s1, s2}, width);
+}
+
 int32_t dcp_kv_append(const dcp_paged_kv *kv, const void *k_new, const void *v_new, const int32_t *seq_lens,
                       const int32_t *query_start_loc, int64_t T, int32_t num_reqs, int64_t k_stride_t,
                       int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h, int32_t shard, int32_t num_shards,
@@ -337,7 +371,7 @@ int32_t dcp_kv_weights(const float *logits, const float *global_lse, const int32
     if (!logits || !global_lse || !seq_lens || !weights) return fail(DCP_ERR_INVALID_ARG, "%s: null buffer pointer", fn);
     if (!aligned(logits, 4) || !aligned(global_lse, 4) || !aligned(seq_lens, 4) || !aligned(weights, 4))
         return fail(DCP_ERR_MISALIGNED, "%s: all arrays must be 4-byte aligned", fn);
-    if (rows_overlap(B, weights_stride_b, heads, weights_stride_h, cap))
+    if (rows_overlap({B, heads, 1}, {weights_stride_b, weights_stride_h, 0}, cap))
         return fail(DCP_ERR_INVALID_ARG, "%s: the rows of weights overlap", fn);
     a.logits = logits;
     a.lse = global_lse;
@@ -387,7 +421,7 @@ int32_t dcp_kv_evict(const dcp_paged_kv *src, const dcp_paged_kv *dst, const int
     if (!aligned(seq_lens, 4) || !aligned(weights, 4) || !aligned(new_weights, 4) || !aligned(kept, 4) ||
         !aligned(new_lens, 4))
         return fail(DCP_ERR_MISALIGNED, "%s: all arrays must be 4-byte aligned", fn);
-    if (rows_overlap(B, new_weights_stride_b, dst->heads, new_weights_stride_h, new_cap))
+    if (rows_overlap({B, dst->heads, 1}, {new_weights_stride_b, new_weights_stride_h, 0}, new_cap))
         return fail(DCP_ERR_INVALID_ARG, "%s: the rows of new_weights overlap", fn);
     a.seq_lens = seq_lens;
     a.weights = weights;

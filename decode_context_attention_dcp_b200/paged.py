@@ -62,6 +62,8 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.dcp_testing_paged_attention_stalled.restype = _i32
     lib.dcp_testing_paged_attention_resident.argtypes = [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32)]
     lib.dcp_testing_paged_attention_resident.restype = _i32
+    lib.dcp_testing_rows_overlap.argtypes = [_i64] * 7
+    lib.dcp_testing_rows_overlap.restype = _i32
     lib.dcp_kv_append.argtypes = [kv, _ptr, _ptr, _ptr, _ptr, _i64, _i32, _i64, _i64, _i64, _i64, _i32, _i32, _i32,
                                   _ptr]
     lib.dcp_kv_append.restype = _i32

@@ -62,7 +62,7 @@ extern "C" {
  * 16 bytes; heads in [1, DCP_MAX_PAGED_HEADS]; page_size >= 1; num_pages >= 0; max_pages >= 0; max_pages * page_size
  * < 2^31 - 1024; k and v 16-byte aligned; strides >= 0 and multiples of 16 bytes; block_table 4-byte
  * aligned, entry (b, j) at b*table_stride + j.  In a cache that a call writes (append, evict's dst) the
- * rows must not overlap; strides below head_dim, of a dimension of two or more entries, are refused.
+ * rows must not overlap; strides (of dimensions of two or more entries) under which they do are refused.
  */
 typedef struct {
     void *k;
@@ -113,8 +113,8 @@ int64_t dcp_paged_attention_workspace(int64_t H, int32_t heads, int32_t head_dim
  * lse         [B, H] fp32, contiguous.
  * logits      NULL, or fp32: x_p of head h goes to b*logits_stride_b + h*logits_stride_h + p for
  *             the held positions p < logits_cap (the others are left as they were; a position
- *             in a page outside the pool gets -inf).  Its rows must not overlap: strides below
- *             logits_cap are refused (B or H of 1: its stride does not matter).
+ *             in a page outside the pool gets -inf).  Its rows must not overlap: strides under which
+ *             rows of logits_cap do are refused (B or H of 1: its stride does not matter).
  * workspace   at least dcp_paged_attention_workspace bytes, 16-byte aligned; its contents need no
  *             initialisation and mean nothing afterwards.  Calls that may run at the same time
  *             need one each.
@@ -184,8 +184,7 @@ int32_t dcp_kv_append(const dcp_paged_kv *kv, const void *k_new, const void *v_n
  * weights     fp32, updated in place; element (b, j, p) at b*weights_stride_b + j*weights_stride_h + p.
  *
  * Requirements: B >= 0; heads >= 1; H a multiple of heads (else DCP_ERR_SHAPE); cap in [0, 2^31);
- * strides >= 0; the rows of weights must not overlap (strides below cap are refused where there is more
- * than one row); all pointers 4-byte aligned; B*H < 2^31.
+ * strides >= 0; the rows of weights must not overlap (strides under which they do are refused); all pointers 4-byte aligned; B*H < 2^31.
  */
 int32_t dcp_kv_weights(const float *logits, const float *global_lse, const int32_t *seq_lens, float *weights,
                        int64_t B, int64_t H, int64_t heads, int64_t cap, int64_t logits_stride_b,
@@ -212,8 +211,8 @@ int32_t dcp_kv_weights(const float *logits, const float *global_lse, const int32
  * weights     fp32 [B, heads, cap], element (b, j, p) at b*weights_stride_b + j*weights_stride_h + p;
  *             lengths are cut to cap.
  * new_weights fp32 [B, heads, new_cap], strides alike; all new_cap entries are written; new_cap
- *             >= keep.  Must not overlap weights, nor its rows one another (strides below new_cap
- *             are refused).
+ *             >= keep.  Must not overlap weights, nor its rows one another (strides under which they
+ *             do are refused).
  * kept        [B, heads, keep] int32, contiguous: the kept positions, then -1.
  * new_lens    [B] int32: min(n, keep).
  *

@@ -3,7 +3,8 @@
  * kernels' and of the paged attention's bounded waits run, so that a test can check them without
  * faulting or hanging a GPU; one reports the launch shape the host picks for a split-layout combine, so that the
  * shape rules can be checked without a GPU; two report which pack kernel ran and the tensor
- * pack's tile shape; one how many blocks of the paged attention an SM holds.  Not part of the combine; no page has a counterpart.
+ * pack's tile shape; one how many blocks of the paged attention an SM holds, one
+ * which outputs of the paged calls are refused for overlapping rows.  Not part of the combine; no page has a counterpart.
  */
 #ifndef DCP_TESTING_H
 #define DCP_TESTING_H
@@ -51,6 +52,13 @@ int32_t dcp_testing_paged_attention_stalled(const dcp_paged_kv *kv, const void *
  */
 int32_t dcp_testing_paged_attention_resident(int32_t group, int32_t head_dim, int32_t dtype, int32_t page_size,
                                              int32_t cluster, int32_t *out);
+
+/*
+ * Whether the paged calls refuse an output of n0 x n1 x n2 rows of `width` elements with these strides (>= 0)
+ * because rows share elements: 1 or 0.  Needs no GPU.
+ */
+int32_t dcp_testing_rows_overlap(int64_t n0, int64_t n1, int64_t n2, int64_t s0, int64_t s1, int64_t s2,
+                                 int64_t width);
 
 /*
  * The shape the host picks for a split-layout combine of N shards whose rows are `chunks`
