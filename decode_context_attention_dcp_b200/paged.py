@@ -116,11 +116,11 @@ def _done(status) -> bool:
     return status is not None
 
 
-def _check_ints(**values) -> None:
-    """Arguments that the C ABI takes as 32-bit integers (ctypes would cut them)."""
+def _check_ints(bits: int = 32, **values) -> None:
+    """Arguments that the C ABI takes as integers of so many bits (ctypes would cut them)."""
     for what, n in values.items():
-        if not -(1 << 31) <= n < 1 << 31:
-            raise ValueError(f"{what}={n} is outside the range of 32-bit integers")
+        if not -(1 << bits - 1) <= n < 1 << bits - 1:
+            raise ValueError(f"{what}={n} is outside the range of {bits}-bit integers")
 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, requests: int,
@@ -363,6 +363,7 @@ def dcp_kv_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     dev = _cuda(weights, k_cache, v_cache, block_table, seq_lens, k_out, v_out, new_block_table, kept, new_lens,
                 new_weights)
     _check_ints(shard=shard, num_shards=num_shards, interleave=interleave)
+    _check_ints(64, keep=keep, recent=recent)
     B = seq_lens.numel()
     _lens(seq_lens, B)
     src = _cache(k_cache, v_cache, block_table, B)

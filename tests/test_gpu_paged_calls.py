@@ -62,3 +62,14 @@ def test_the_same_results_without_the_compiled_binding(monkeypatch):
     monkeypatch.setattr(paged, "_native", paged._NoBinding)
     for a, b in zip(step(), want):
         assert torch.equal(a, b)
+
+
+def test_eviction_refuses_integers_past_64_bits():
+    k = torch.zeros(8, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    w, table, new = torch.rand(1, 2, 40, device="cuda"), i32([[0, 1, 2]]), i32([[4, 5]])
+    for recent in ((1 << 64) + 1, -(1 << 64) + 1):
+        with pytest.raises(ValueError, match="64-bit"):
+            dcp.kv_evict(w, k, k.clone(), table, i32([40]), new, 20, recent)
+    for recent in (1 << 40, 21, -1):
+        with pytest.raises(dcp.DCPError, match="recent"):
+            dcp.kv_evict(w, k, k.clone(), table, i32([40]), new, 20, recent)
