@@ -14,7 +14,15 @@ and, when the local cache is over its budget,
     kept, new_lens, weights = kv_evict(weights, k_cache, v_cache, block_table, seq_lens, new_block_table, keep, recent,
                                        shard=r, num_shards=N)
 
-after which new_lens are this rank's lengths (num_shards = 1).
+after which new_lens are this rank's lengths (num_shards = 1).  A token that follows goes to the rank
+that owns its position p in the request, (p // interleave) % N, and only there: that rank's length grows by one,
+and in dcp_kv_append a length of 0 leaves out the token of a request.  On the device, with `lens` this
+rank's lengths and `total` the requests' lengths with the new token:
+
+    own = (total - 1) // interleave % N == r
+    lens += own
+    dcp_kv_append(k_new, v_new, k_cache, v_cache, block_table, torch.where(own, lens, 0), query_start_loc)
+    send = paged_attention_pack(q, k_cache, v_cache, block_table, lens, N, logits=logits)
 
 The cache is any pair of [pages, page_size, heads, D] views whose last dimension is contiguous
 (permute a [pages, heads, page_size, D] pool); local position p of request b is slot p % page_size

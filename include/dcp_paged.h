@@ -157,7 +157,8 @@ int32_t dcp_paged_attention_pack(const dcp_paged_kv *kv, const void *q, const in
  * an order: the key row may hold parts of both, and the value row another mixture.
  *
  * k_new, v_new  [T, heads, head_dim] of kv->dtype; element (t, h, d) at t*stride_t + h*stride_h + d.
- * seq_lens      [num_reqs] int32, device: lengths over all shards, the new tokens included.
+ * seq_lens      [num_reqs] int32, device: lengths over all shards, the new tokens included (a length of 0
+ *               leaves out the request's tokens, as after an eviction those that another rank owns).
  * query_start_loc [num_reqs + 1] int32, device, non-decreasing (other values give unspecified
  *               rows but no access outside the arrays).
  *

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import decode_context_attention_dcp_b200 as dcp
+import paged_ref as ref
 from decode_context_attention_dcp_b200 import paged
+from test_gpu_paged_cache import check_evict
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +75,48 @@ def test_eviction_refuses_integers_past_64_bits():
     for recent in (1 << 40, 21, -1):
         with pytest.raises(dcp.DCPError, match="recent"):
             dcp.kv_evict(w, k, k.clone(), table, i32([40]), new, 20, recent)
+
+
+@pytest.mark.parametrize("interleave", [1, 3])
+def test_tokens_that_follow_an_eviction_in_a_captured_step(interleave):
+    """Ranks of lengths of their own: a step captured once, in which each rank appends the tokens it owns (lengths of
+    0 leave the others out), replayed for twelve tokens."""
+    N, R, heads, D, page = 2, 3, 2, 64, 4
+    total = i32([7, 20, 1])
+    k_new, v_new = (torch.zeros(R, heads, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ranks = []
+    for r in range(N):
+        k = torch.full((18, page, heads, D), -1.0, dtype=torch.bfloat16, device="cuda")
+        ranks.append(dict(k=k, v=k.clone(), lens=i32([2 + r, 5, 0]), table=torch.arange(18, dtype=torch.int32,
+                                                                                       device="cuda").reshape(R, 6)))
+    starts = i32(list(range(R + 1)))
+
+    def step():
+        total.add_(1)
+        for r, c in enumerate(ranks):
+            own = (total - 1) // interleave % N == r
+            c["lens"] += own
+            dcp.dcp_kv_append(k_new, v_new, c["k"], c["v"], c["table"], torch.where(own, c["lens"], 0), starts)
+
+    held = [[[-1.0] * int(n) for n in c["lens"]] for c in ranks]  # per rank and request: the values of its slots
+    first = total.tolist()
+    warm = torch.cuda.Stream()
+    with torch.cuda.stream(warm):
+        dcp.dcp_kv_append(k_new, v_new, ranks[0]["k"], ranks[0]["v"], ranks[0]["table"], i32([0] * R), starts)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(12):
+        k_new.copy_((torch.arange(R) + 1 + 10 * i)[:, None, None].expand(R, heads, D))
+        v_new.copy_(k_new + 1)
+        graph.replay()
+        for b in range(R):
+            held[(first[b] + i) // interleave % N][b].append(float(b + 1 + 10 * i))
+    for r, c in enumerate(ranks):
+        assert c["lens"].tolist() == [len(x) for x in held[r]]
+        for b in range(R):
+            for pool, more in (("k", 0), ("v", 1)):
+                slots = c[pool][6 * b:6 * b + 6].reshape(6 * page, heads, D).float()
+                want = [x + more * (x > 0) for x in held[r][b]] + [-1.0] * (6 * page - len(held[r][b]))
+                assert (slots == torch.tensor(want, device="cuda")[:, None, None]).all(), (r, b, pool)
