@@ -120,3 +120,40 @@ def test_tokens_that_follow_an_eviction_in_a_captured_step(interleave):
                 slots = c[pool][6 * b:6 * b + 6].reshape(6 * page, heads, D).float()
                 want = [x + more * (x > 0) for x in held[r][b]] + [-1.0] * (6 * page - len(held[r][b]))
                 assert (slots == torch.tensor(want, device="cuda")[:, None, None]).all(), (r, b, pool)
+
+
+@pytest.mark.parametrize("lens,seq", [([0, 100], [-3, 1 << 30]), ([0, 100] * 115, [-(1 << 31), (1 << 31) - 1] * 115),
+                                      ([20011, 0, 20011], [20012, -1, 1 << 30]), ([0, 60000], [-5, 1 << 30])])
+def test_eviction_of_negative_lengths_and_lengths_past_the_arrays(lens, seq):
+    """In every selection kernel: a negative length is 0 (nothing kept, new weights all 0), a longer one is cut."""
+    check_evict(lens, 2 if len(lens) < 10 else 4, 8, 16, 40, 5, seq=seq)
+    check_evict(lens, 1, 8, 64, 40, 5, seq=seq, new_cap=47)
+
+
+@pytest.mark.parametrize("n,keep,wide", [(n, keep, wide) for n, keep in ((100, 30), (3000, 500), (20000, 1000), (5, 40))
+                                         for wide in (4097, 49153, 131072) if wide > n])
+def test_eviction_in_arrays_wider_than_their_content(n, keep, wide):
+    """Weights and tables with room for far more positions than are held, as a server keeps them: the same as
+    in arrays of the content's size."""
+    heads, page, lens = 2, 16, [n, n // 2, 0]
+    case = ref.PagedCase(lens, heads, 16, page, "bf16", seed=n)
+    k, v, table = case.gpu()
+    w = torch.rand(3, heads, n, generator=torch.Generator().manual_seed(n)).cuda()
+    new = torch.randperm(3 * (keep // page + 1), generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    new = new.reshape(3, -1).cuda()
+    w_wide = torch.full((3, heads, wide), float("nan"), device="cuda")  # not held: never looked at
+    w_wide[:, :, :n] = w
+    t_wide = torch.full((3, wide // page + 1), -1, dtype=torch.int32, device="cuda")
+    t_wide[:, :table.shape[1]] = table
+    t_new = torch.full((3, wide // page + 1), -1, dtype=torch.int32, device="cuda")
+    t_new[:, :new.shape[1]] = new
+    results = []
+    for weights, src, dst in ((w, table, new), (w_wide, t_wide, t_new)):
+        ko = torch.zeros(new.numel(), page, heads, 16, dtype=k.dtype, device="cuda")
+        vo = torch.zeros_like(ko)
+        kept, nl, nw = dcp.kv_evict(weights, k, v, src, i32(lens), dst, keep, keep // 8, k_out=ko, v_out=vo)
+        results.append((kept, nl, ko, vo, nw))
+    for a, b in zip(results[0][:4], results[1][:4]):
+        assert torch.equal(a, b)
+    assert torch.equal(results[1][4][:, :, :results[0][4].shape[2]], results[0][4])
+    assert (results[1][4][:, :, results[0][4].shape[2]:] == 0).all()
