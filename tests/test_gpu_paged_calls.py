@@ -157,3 +157,27 @@ def test_eviction_in_arrays_wider_than_their_content(n, keep, wide):
         assert torch.equal(a, b)
     assert torch.equal(results[1][4][:, :, :results[0][4].shape[2]], results[0][4])
     assert (results[1][4][:, :, results[0][4].shape[2]:] == 0).all()
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 20), (256, 16)])
+def test_long_fp32_sums_keep_their_precision(D, page):
+    """512 requests that share 20011 positions: some 300 tiles per block, so sums of thousands of positions.
+
+    The error's RMS relative to the result's, from the arithmetic, each part independent and of random sign: a
+    logit's products with factors of two tf32 parts, the second cut to 10 bits (up to 2^-21 of a factor, RMS half
+    of it over sqrt(3) each, twice): 2e-7 of a logit of standard deviation 1; its sum's roundings, about 8 of
+    2^-24: 2e-7; exp2 and its argument, 2^-22 and 2^-24 times 8: 4e-7 together; weight and value in the product,
+    2e-7; the fp32 sums of 360 tiles, a random walk of 2^-25: 19 times 3e-8 of a sum that itself grows as one:
+    4e-7.  In all 7e-7; the bound is 2e-6.  (The same sums left to the product units: 5e-6; products of one
+    tf32 part: 1e-4.)"""
+    B, n = 512, 20011
+    case = ref.PagedCase([n], 1, D, page, "fp32", seed=D + page)
+    k, v, table = case.gpu()
+    q = torch.randn(B, 2, D, generator=torch.Generator().manual_seed(D)).cuda()
+    out, lse = dcp.paged_attention(q, k, v, table.expand(B, -1), i32([n] * B))
+    keys, values = case.keys[0][:, 0].double().cuda(), case.values[0][:, 0].double().cuda()
+    x = q.double().reshape(2 * B, D) @ keys.t() * (1 / D ** 0.5)
+    want = (x.softmax(1) @ values).reshape(B, 2, D)
+    assert float((out.double() - want).norm() / want.norm()) <= 2e-6
+    # ln of a sum whose terms have relative errors of 1e-6 at most, rounded at its size of about 10.4
+    assert float((lse.double() - x.logsumexp(1).reshape(B, 2)).abs().max()) <= 1e-6 + 4 * 2.0 ** -21
