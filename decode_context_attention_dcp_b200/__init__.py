@@ -115,8 +115,9 @@ def dcp_last_error() -> str:
 
 
 def dcp_wait_timeouts(reset: bool = False) -> int:
-    """Pack CTAs whose wait for their copies timed out on the current device since the last
-    reset (synchronises the device).  Nonzero means some dcp_pack result is incomplete."""
+    """Pack CTAs and paged-attention warps whose wait for their copies timed out on the current device
+    since the last reset (synchronises the device).  Nonzero means some dcp_pack result is incomplete or
+    some paged attention's is not valid."""
     c = ctypes.c_uint64(0)
     _check(library().dcp_wait_timeouts(ctypes.byref(c), int(bool(reset))))
     return int(c.value)

@@ -4,17 +4,19 @@
 // K and V with the running maximum and sum of the softmax.
 //
 // What bounds it.  A position costs 2 D elements of K and V per key head and 4 G D flops for the G
-// query heads that share it: G flops per byte (16-bit), far below the machine's balance for any
-// group of this size, so the kernel is a stream over the held pages and everything else is
+// query heads that share it: G flops per byte (16-bit), far below the machine's balance for groups of up to
+// 16 heads, so the kernel is a stream over the held pages and everything else is
 // arranged to keep that stream full.  The products run on mma.sync (m16n8k16, fp32 sums) with
 // positions (x = K q^T) and then columns (o^T = V^T p^T) as the 16 rows and query heads as the 8 columns, so
 // that a group of up to 8 heads costs one product per 16 x 16 block of K or V.  Operands come
 // straight from the streamed tile.  tcgen05 would want 128 rows per product and an operand round
-// trip through tensor memory, for a pipe that is idle most of the time either way.
+// trip through tensor memory, for a pipe that is idle most of the time either way (14% busy with 8 heads, 27% with
+// 16).  Wider groups are not covered by that: above 32 heads K and V are streamed once per block of heads
+// (8 requests of 131072, one key head, D = 128, bf16, 82 us of bytes: 8 heads 94 us, 16 102, 32 112, 64 203, 128 385).
 //
 // Measured (device time; share of the 6548 GB/s copy rate of the bytes that have to move): 128 requests of 2048 to
-// 8192 positions, 128 heads on 8, D = 128, bf16: 421 us, 96% (436 us, 92%, after seconds of it under the power
-// cap); 64 of 0 to 8192, 64 heads on 8: 178 us, 93%; 3 of 100000 to 131072, 64 heads on 4, fp16: 127 us, 87%; one of
+// 8192 positions, 128 heads on 8, D = 128, bf16: 422 us, 96% (437 us, 92%, after seconds of it under the power
+// cap); 64 of 0 to 8192, 64 heads on 8: 179 us, 93%; 3 of 100000 to 131072, 64 heads on 4, fp16: 128 us, 87%; one of
 // 777, 32 heads on 8: 5.9 us.  SMs get bandwidth that differs by up to 15%, so the first CTAs of a
 // wave end that much before the last; cutting the end of the work into smaller shares gained 2% on the
 // second case and cost 11% on the third.
@@ -1253,7 +1255,9 @@ namespace dcp_host {
 
 // CTAs per request, key head and head block of a short call, 0 where the tiles are shared evenly
 // instead: as many as leave all of them resident, at most 8 and at most one per tile of the longest
-// request that the table can hold, if each then has at most kClusterTiles tiles.
+// request that the table can hold, if each then has at most kClusterTiles tiles.  One request of 777, 32
+// heads on 8: 6.9 us so, 8.0 with the tiles shared evenly; 24 of 181, 32 heads on 4: 8.7 and 9.8.  The
+// host sees the table's width and not the lengths, so a wide table brings the second form to short requests.
 constexpr int64_t kClusterTiles = 4;
 
 inline int cluster_size(int64_t segments, int64_t tiles, int64_t most) {
@@ -1352,7 +1356,7 @@ int32_t launch_attention(const dcp::AttentionArgs &a, cudaStream_t stream) {
 // room for 12 (D = 256: 6) warps of one stage or half as many of two, and computes for so long that the
 // number of warps counts: a stage is not refilled while its warp computes, but the other warps' copies
 // run.  24 requests of 3000, 12 heads on 4, one stage against two: D = 128 59.7 / 65.6 us, D = 256 129 / 176;
-// 64 heads on 4, D = 128: 79 / 92.  For 16-bit types of D = 256 the exchange does not pay (54.5 / 55 us; 64 heads
+// 64 heads on 4, D = 128: 80 / 92 (pages of 20 slots: 87).  For 16-bit types of D = 256 the exchange does not pay (54.5 / 55 us; 64 heads
 // on 4: 89 / 59).
 template <class T, class F>
 auto with_shape(int32_t group, int32_t head_dim, F &&f) {

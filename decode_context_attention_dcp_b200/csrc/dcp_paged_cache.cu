@@ -83,7 +83,7 @@ __device__ __forceinline__ int request_of(const AppendArgs &a, int t) {
     return lo - 1;
 }
 
-// 8192 rows of 8 heads x 256 bytes (67 MB moved): 14.1 us, 4.7 TB/s; 256 single tokens: 3 us, four
+// 8192 rows of 8 heads x 256 bytes (67 MB moved): 15.0 us, 4.5 TB/s; 256 single tokens: 3.1 us, four
 // dependent reads (start, length, page, row).
 // A block takes `per` <= 32 tokens at a time: lane i of its first warp finds the place of token i,
 // the tokens that this rank holds are put together, and the whole block copies their rows, all
@@ -279,7 +279,11 @@ __device__ __forceinline__ RowMove place(const EvictArgs &a, int b, int h, int32
 //   kShared     one CTA, in shared memory: longer rows without a second reading;
 //   kCluster    a cluster of CTAs, in registers; what they cannot hold is read again per pass.
 // Measured at 256 rows of 20000 to 32768 weights (27 MB read, as much written): kShared 40 us in two
-// waves of 148 CTAs, kCluster (4 CTAs, a barrier and remote histograms per pass) 72 us.  At 24
+// waves of 148 CTAs, kCluster (4 CTAs, a barrier and remote histograms per pass) 72 us.  Few rows do not
+// turn that round: whole calls with 4096 kept (kCluster with 8 CTAs), 8 rows of 8192 15.9 / 32.6 us, of 32768 25.6 /
+// 30.2; 32 rows 33.9 / 78.0 and 44.3 / 73.7; 256 rows of 32768 215 / 530.  So kCluster is left with the rows that
+// shared memory cannot hold, by the arrays' width (the host does not see the lengths): 256 rows of
+// 32768 in arrays of 131072 take 540 us.  At 24
 // rows of up to 2000: 6.9 us with 256 threads, 9.3 us with 1024.  Bound by the chain load,
 // three histograms and prefix sums, output (16 us per CTA), not by bytes.
 enum KeyStore { kRegisters, kShared, kCluster };
@@ -669,7 +673,7 @@ int32_t kv_evict(const dcp::EvictArgs &a, cudaStream_t stream) {
     const int64_t parts = (a.keep - 1) / dcp::kMoveRows + 1;
     cudaError_t e;
     if (longest <= 256 * dcp::kKeys && rows * parts <= 3 * sm_count()) {
-        // all of it at once on the device: every CTA selects for itself (24 rows of up to 2000, 512 kept: 8.8 us,
+        // all of it at once on the device: every CTA selects for itself (24 rows of up to 2000, 512 kept: 9.1 us,
         // selection and moves apart 10.6; 512 CTAs for 128 rows of 4000: 16.1 against 15.0)
         if (launch_select<256, dcp::kRegisters, true>(a, (int)parts, 0, stream) != cudaSuccess)
             return launch_status("dcp_kv_evict");
