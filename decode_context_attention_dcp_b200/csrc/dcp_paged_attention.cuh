@@ -444,8 +444,11 @@ __global__ void __launch_bounds__(S::kThreads, S::CTAS)
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    asm volatile("griddepcontrol.launch_dependents;");
-    if (!CLUSTER && tid == 0) s_mend = 0;
+    if constexpr (!CLUSTER) {
+        // the join may be launched; a cluster's results are final, what follows it has to wait for its end
+        asm volatile("griddepcontrol.launch_dependents;");
+        if (tid == 0) s_mend = 0;
+    }
     constexpr bool TENSOR = S::BOX > 0;
     if (TENSOR && lane == 0) {
         for (int st = 0; st < ST; ++st) mbar_init(&s_full[warp][st], 1);

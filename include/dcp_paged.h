@@ -97,7 +97,7 @@ int64_t dcp_paged_attention_workspace(int64_t H, int32_t heads, int32_t head_dim
  * A position whose logit is -inf adds nothing (16-bit types), a row whose logits are all -inf counts as
  * empty.  A value that is not finite gives its column what IEEE products with the weights give: infinities
  * of one sign that infinity; a NaN, both signs, or an infinity whose weight is 0 (a logit of -inf, or
- * one 88 or more below the row's largest) NaN.  A row that meets a non-finite fp32 key is NaN; fp32 keys
+ * one some 90 or more below the row's largest) NaN.  A row that meets a non-finite fp32 key is NaN; fp32 keys
  * and values of magnitude 2^128 - 2^116 or more make NaN of their row, or of their column.
  * For 16-bit types exp(x_p - m) is carried into the product with v as two 16-bit parts; fp32
  * products are formed from two tf32 parts of each factor (2^-20 of the product).
